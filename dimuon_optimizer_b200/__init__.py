@@ -40,6 +40,9 @@ DM_SCALE_NONE = 0
 DM_SCALE_MOONSHOT = 1
 DM_SCALE_JORDAN = 2
 DM_SCALE_BERNSTEIN = 3
+DM_STATE_FP32 = 0
+DM_STATE_8BIT = 1
+DM_ADAMW_BLOCK = 128
 DM_THIN_MAX = 32
 DM_MAX_NS_STEPS = 64
 DM_DBG_NO_THIN = 0x1
@@ -55,8 +58,9 @@ DM_DBG_CANARY_SELFTEST = 0x100
 DM_NOALLOC_MAX_BYTES = 32 * 1024 * 1024
 
 EXPORTED = ("dm_default_hparams", "dm_workspace_size", "dm_step_launches", "dm_muon_step",
-            "dm_dimuon_step", "dm_read_device_status", "dm_step_noalloc", "dm_status_string",
-            "dm_version")
+            "dm_dimuon_step", "dm_read_device_status", "dm_step_noalloc",
+            "dm_adamw_default_hparams", "dm_adamw_workspace_size", "dm_adamw_step",
+            "dm_grad_clip_workspace_size", "dm_grad_clip", "dm_status_string", "dm_version")
 
 
 class dm_matrix_t(ctypes.Structure):
@@ -72,6 +76,26 @@ class dm_hparams_t(ctypes.Structure):
                 ("cond_eps", c_float), ("scale_mode", c_int32), ("scale_coef", c_float),
                 ("precision", c_int32), ("debug_flags", c_uint32), ("nesterov", c_int32),
                 ("reserved", c_int32 * 3), ("ns_coeffs", ctypes.POINTER(c_float))]
+
+
+class dm_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [("numel", c_int64), ("weight", c_void_p), ("grad", c_void_p),
+                ("moment1", c_void_p), ("moment2", c_void_p), ("scale1", c_void_p),
+                ("scale2", c_void_p), ("weight_dtype", c_int32), ("grad_dtype", c_int32),
+                ("state", c_int32), ("lr_mult", c_float), ("decay_mult", c_float),
+                ("reserved0", c_int32)]
+
+
+class dm_adamw_hparams_t(ctypes.Structure):
+    _fields_ = [("lr", c_float), ("beta1", c_float), ("beta2", c_float), ("eps", c_float),
+                ("weight_decay", c_float), ("seed", c_uint32), ("step", c_int64),
+                ("step_counter", c_void_p), ("lr_dev", c_void_p), ("grad_scale", c_void_p),
+                ("reserved", c_int32 * 2)]
+
+
+class dm_grad_t(ctypes.Structure):
+    _fields_ = [("numel", c_int64), ("grad", c_void_p), ("out", c_void_p),
+                ("grad_dtype", c_int32), ("out_dtype", c_int32)]
 
 
 class DimuonError(RuntimeError):
@@ -101,6 +125,19 @@ def _load():
     lib.dm_step_noalloc.argtypes = [P(dm_matrix_t), c_int, P(dm_hparams_t), c_int, c_void_p,
                                     c_void_p]
     lib.dm_step_noalloc.restype = c_int
+    lib.dm_adamw_default_hparams.argtypes = [P(dm_adamw_hparams_t)]
+    lib.dm_adamw_default_hparams.restype = None
+    lib.dm_adamw_workspace_size.argtypes = [P(dm_adamw_tensor_t), c_int, P(dm_adamw_hparams_t),
+                                            P(c_size_t)]
+    lib.dm_adamw_workspace_size.restype = c_int
+    lib.dm_adamw_step.argtypes = [P(dm_adamw_tensor_t), c_int, P(dm_adamw_hparams_t), c_void_p,
+                                  c_size_t, c_void_p]
+    lib.dm_adamw_step.restype = c_int
+    lib.dm_grad_clip_workspace_size.argtypes = [P(dm_grad_t), c_int, P(c_size_t)]
+    lib.dm_grad_clip_workspace_size.restype = c_int
+    lib.dm_grad_clip.argtypes = [P(dm_grad_t), c_int, c_float, c_void_p, c_void_p, c_size_t,
+                                 c_void_p]
+    lib.dm_grad_clip.restype = c_int
     lib.dm_read_device_status.argtypes = [c_void_p, c_void_p, P(c_int32)]
     lib.dm_read_device_status.restype = c_int
     lib.dm_status_string.argtypes = [c_int32]
@@ -158,6 +195,13 @@ def _array(mats):
     mats = list(mats)
     arr = (dm_matrix_t * max(1, len(mats)))(*mats)
     return arr, len(mats)
+
+
+def _list(items, struct):
+    if isinstance(items, ctypes.Array):
+        return items, len(items)
+    items = list(items)
+    return (struct * max(1, len(items)))(*items), len(items)
 
 
 def _stream_handle(stream):
@@ -249,6 +293,158 @@ def dm_step_noalloc(mats, hp, conditioned, device_status_out=None, stream=None):
     arr, n = _array(mats)
     return _lib.dm_step_noalloc(arr, n, ctypes.byref(hp), int(conditioned),
                                 _ptr(device_status_out), _stream_handle(stream))
+
+
+# ----------------------------------------------------------------------------
+# AdamW over many tensors, gradient clipping
+# ----------------------------------------------------------------------------
+def _on_device(*tensors):
+    """All on the current CUDA device and contiguous, else ValueError (a host
+    or foreign address would fault in the kernels)."""
+    import torch
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}: needs the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+
+def dm_adamw_state(weight, state=DM_STATE_FP32):
+    """Zero moments for `weight`: (moment1, moment2) in fp32, or (moment1,
+    moment2, scale1, scale2) with DM_STATE_8BIT; pass them to dm_adamw_tensor
+    after weight and grad.  A moment's value is code.float() times its
+    block's scale."""
+    import torch
+    if state == DM_STATE_FP32:
+        return tuple(torch.zeros(weight.shape, dtype=torch.float32, device=weight.device)
+                     for _ in range(2))
+    if state != DM_STATE_8BIT:
+        raise ValueError(f"unknown state format {state}")
+    blocks = -(-weight.numel() // DM_ADAMW_BLOCK)
+    return (torch.zeros(weight.shape, dtype=torch.uint8, device=weight.device)
+            .view(torch.float8_e4m3fn),
+            torch.zeros(weight.shape, dtype=torch.uint8, device=weight.device)
+            .view(torch.float8_e5m2),
+            torch.zeros(blocks, dtype=torch.float32, device=weight.device),
+            torch.zeros(blocks, dtype=torch.float32, device=weight.device))
+
+
+def dm_adamw_tensor(weight, grad, moment1, moment2, scale1=None, scale2=None, lr_mult=1.0,
+                    decay_mult=1.0):
+    """A dm_adamw_tensor_t over contiguous torch CUDA tensors of one size.
+    The moments are fp32, or float8_e4m3fn and float8_e5m2 with one fp32
+    scale per DM_ADAMW_BLOCK elements (scale1, scale2)."""
+    import torch
+    n = weight.numel()
+    if any(t.numel() != n for t in (grad, moment1, moment2)):
+        raise ValueError("weight, grad and moments must have the same number of elements")
+    kinds = (moment1.dtype, moment2.dtype)
+    t = dm_adamw_tensor_t()
+    if kinds == (torch.float32, torch.float32):
+        if scale1 is not None or scale2 is not None:
+            raise ValueError("fp32 moments take no scales")
+        t.state = DM_STATE_FP32
+    elif kinds == (torch.float8_e4m3fn, torch.float8_e5m2):
+        blocks = -(-n // DM_ADAMW_BLOCK)
+        for s in (scale1, scale2):
+            if s is None or s.numel() != blocks or s.dtype != torch.float32:
+                raise ValueError(f"8-bit moments need fp32 scales of {blocks} blocks")
+        t.state = DM_STATE_8BIT
+        t.scale1, t.scale2 = scale1.data_ptr(), scale2.data_ptr()
+    else:
+        raise TypeError(f"unsupported moments {kinds} (fp32, or float8_e4m3fn and float8_e5m2)")
+    t.weight_dtype, t.grad_dtype = _dtype_code(weight), _dtype_code(grad)
+    _on_device(weight, grad, moment1, moment2, scale1, scale2)
+    t.numel = n
+    t.weight, t.grad = weight.data_ptr(), grad.data_ptr()
+    t.moment1, t.moment2 = moment1.data_ptr(), moment2.data_ptr()
+    t.lr_mult, t.decay_mult = lr_mult, decay_mult
+    return t
+
+
+def dm_adamw_tensors(tensors):
+    """The descriptors as one C array, for callers that keep it from step to
+    step (a plain list is converted at every call)."""
+    return _list(tensors, dm_adamw_tensor_t)[0] if len(tensors) else []
+
+
+def dm_adamw_default_hparams(**overrides):
+    """dm_adamw_hparams_t with the library's defaults and the given fields
+    set.  step_counter (int64), lr_dev and grad_scale (fp32) take one-element
+    CUDA tensors, which the struct keeps alive."""
+    import torch
+    hp = dm_adamw_hparams_t()
+    _lib.dm_adamw_default_hparams(ctypes.byref(hp))
+    hp._keep = []
+    for k, v in overrides.items():
+        if k in ("step_counter", "lr_dev", "grad_scale") and v is not None:
+            want = torch.int64 if k == "step_counter" else torch.float32
+            if v.numel() != 1 or v.dtype != want:
+                raise ValueError(f"{k} must be one {want} element on the device")
+            _on_device(v)
+            hp._keep.append(v)
+            v = v.data_ptr()
+        setattr(hp, k, v)
+    return hp
+
+
+def dm_adamw_workspace_size(tensors, hp):
+    arr, n = _list(tensors, dm_adamw_tensor_t)
+    out = c_size_t(0)
+    st = _lib.dm_adamw_workspace_size(arr, n, ctypes.byref(hp), ctypes.byref(out))
+    if st != DM_OK:
+        raise DimuonError(st)
+    return out.value
+
+
+def dm_adamw_step(tensors, hp, workspace, stream=None):
+    """One AdamW step over the tensors (include/dimuon.h).  The caller counts
+    the steps in hp.step, or gives hp a device step_counter."""
+    arr, n = _list(tensors, dm_adamw_tensor_t)
+    ptr, nbytes = _ws(workspace)
+    return _lib.dm_adamw_step(arr, n, ctypes.byref(hp), ptr, nbytes, _stream_handle(stream))
+
+
+def dm_grad_tensor(grad, out=None):
+    """A dm_grad_t over contiguous torch CUDA tensors; `out` (optional, of
+    either dtype, or `grad` itself) gets the clipped gradient."""
+    if out is not None and out.numel() != grad.numel():
+        raise ValueError("grad and out must have the same number of elements")
+    t = dm_grad_t()
+    t.numel, t.grad, t.grad_dtype = grad.numel(), grad.data_ptr(), _dtype_code(grad)
+    if out is not None:
+        t.out, t.out_dtype = out.data_ptr(), _dtype_code(out)
+    _on_device(grad, out)
+    return t
+
+
+def dm_grad_tensors(tensors):
+    """The descriptors as one C array, for callers that keep it."""
+    return _list(tensors, dm_grad_t)[0] if len(tensors) else []
+
+
+def dm_grad_clip_workspace_size(tensors):
+    arr, n = _list(tensors, dm_grad_t)
+    out = c_size_t(0)
+    st = _lib.dm_grad_clip_workspace_size(arr, n, ctypes.byref(out))
+    if st != DM_OK:
+        raise DimuonError(st)
+    return out.value
+
+
+def dm_grad_clip(tensors, max_norm, result, workspace, stream=None):
+    """Global norm of the gradients into result[0], the clip coefficient into
+    result[1] (fp32 CUDA tensor of two), clipped gradients into the outputs."""
+    import torch
+    if result.numel() != 2 or result.dtype != torch.float32:
+        raise ValueError("result must be an fp32 tensor of two elements")
+    _on_device(result)
+    arr, n = _list(tensors, dm_grad_t)
+    ptr, nbytes = _ws(workspace)
+    return _lib.dm_grad_clip(arr, n, float(max_norm), c_void_p(result.data_ptr()), ptr, nbytes,
+                             _stream_handle(stream))
 
 
 def dm_read_device_status(workspace, stream=None):

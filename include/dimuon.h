@@ -293,6 +293,141 @@ dm_status_t dm_step_noalloc(const dm_matrix_t* mats, int n,
                             const dm_hparams_t* hp, int conditioned,
                             int32_t* device_status_out, void* stream);
 
+/* ==========================================================================
+ * The parameters Muon leaves to AdamW, and clipping over both groups.
+ *
+ * Muon takes the 2-D hidden matrices only; embeddings, biases, norms and heads
+ * stay on AdamW (sitech.ge Muon post, "From speedrun to real training").  The
+ * entry points below take a list of flat tensors of any sizes.
+ *
+ * Conventions as above, and:
+ *   - A tensor is `numel` contiguous elements; numel = 0 is allowed (its
+ *     pointers are ignored).  Pointers need the alignment of their element
+ *     type only; buffers whose addresses are at the same element offset from
+ *     a 32-byte boundary (all of them aligned, or views at one offset of flat
+ *     buffers) take the vector path.
+ *   - No element may be written twice in one call: a buffer that appears as an
+ *     output of two tensors is rejected (equal addresses are detected; the
+ *     caller answers for partial overlaps).
+ * ======================================================================== */
+
+/* How a tensor's two moments are held.
+ * DM_STATE_FP32: fp32[numel] each; scale1 and scale2 are ignored.
+ * DM_STATE_8BIT: one byte per element and one fp32 scale per
+ *   DM_ADAMW_BLOCK consecutive elements (the last block may be short): the
+ *   first moment is e4m3 code x scale1, the second e5m2 code x scale2.  A
+ *   scale is the smallest power of two, at least 2^-110, with which the
+ *   block's largest magnitude fits (448 and 57344 times the scale), so code x
+ *   scale is exact.  All-zero codes with any finite scales are the start.
+ *     The codes are rounded stochastically: a moving average changes by
+ *   (1 - beta2) = 0.1 % a step while e5m2 neighbours are 12 to 25 % apart, so
+ *   rounding to nearest would hold it still; the neighbour above is taken
+ *   with the probability of the remainder, from 16 bits of a hash of (seed,
+ *   step, position of the tensor in the call, element), and the average of
+ *   what is stored is the value.  A positive second moment is never rounded
+ *   to zero (its element's next update would be divided by eps alone).
+ *     A block with an infinite or NaN moment gets a NaN scale: the whole block
+ *   stands for NaN from then on, as its element would in DM_STATE_FP32.    */
+typedef enum { DM_STATE_FP32 = 0, DM_STATE_8BIT = 1 } dm_state_t;
+
+#define DM_ADAMW_BLOCK 128
+
+/* One tensor of dm_adamw_step.
+ *   weight       in/out  numel, weight_dtype (bf16: rounded to nearest even)
+ *   grad         in      numel, grad_dtype
+ *   moment1, 2   in/out  as `state` says; all zero before step 1
+ *   scale1, 2    in/out  DM_STATE_8BIT: fp32[ceil(numel / DM_ADAMW_BLOCK)]
+ *   lr_mult, decay_mult  factors of hp.lr and hp.weight_decay for this tensor
+ *                        (0 decay for biases and norms)                    */
+typedef struct {
+  int64_t numel;
+  void* weight;
+  const void* grad;
+  void* moment1;
+  void* moment2;
+  float* scale1;
+  float* scale2;
+  int32_t weight_dtype;
+  int32_t grad_dtype;
+  int32_t state;
+  float lr_mult;
+  float decay_mult;
+  int32_t reserved0;    /* must be zero */
+} dm_adamw_tensor_t;
+
+typedef struct {
+  float lr;
+  float beta1, beta2;   /* in [0, 1) */
+  float eps;            /* >= 0 */
+  float weight_decay;   /* decoupled */
+  uint32_t seed;        /* DM_STATE_8BIT: of the stochastic rounding */
+  int64_t step;         /* t, from 1 on; ignored with step_counter */
+  int64_t* step_counter;  /* NULL, or a DEVICE int64: the number of steps
+                             done.  The step runs as t = *step_counter + 1 and
+                             stores that, so that a captured graph counts its
+                             own replays.  Not advanced by a skipped step. */
+  const float* lr_dev;  /* NULL, or a DEVICE float read in place of lr      */
+  const float* grad_scale;  /* NULL, or a DEVICE float every gradient is
+                             multiplied by (result[1] of dm_grad_clip, or the
+                             inverse of a loss scale)                      */
+  int32_t reserved[2];  /* must be zero */
+} dm_adamw_hparams_t;
+
+/* Fills *hp with the defaults: lr 1e-3, beta1 0.9, beta2 0.999, eps 1e-8,
+ * weight_decay 0.01, seed 0, step 1, no device values. */
+void dm_adamw_default_hparams(dm_adamw_hparams_t* hp);
+
+/* Bytes of device workspace dm_adamw_step needs (256-byte aligned, no
+ * initialisation).  Host-only. */
+dm_status_t dm_adamw_workspace_size(const dm_adamw_tensor_t* tensors, int n,
+                                    const dm_adamw_hparams_t* hp, size_t* bytes);
+
+/* One AdamW step over the tensors, per element, in fp32:
+ *   g  = grad * grad_scale
+ *   m' = beta1 m + (1 - beta1) g
+ *   v' = beta2 v + (1 - beta2) g^2
+ *   W' = (1 - lr wd) W - lr (m' / (1 - beta1^t)) /
+ *                        (sqrt(v' / (1 - beta2^t)) + eps)
+ * (lr and wd with the tensor's multipliers; W' comes from m' and v' before
+ * they are rounded to 8 bits).  Asynchronous on `stream`.
+ * When the device value of grad_scale or lr_dev is not finite, the step is
+ * skipped: nothing but the device status is written, and that reads
+ * DM_ERR_NONFINITE (dm_read_device_status).  Non-finite gradients are not
+ * looked for here: dm_grad_clip finds them and hands over a NaN coefficient. */
+dm_status_t dm_adamw_step(const dm_adamw_tensor_t* tensors, int n,
+                          const dm_adamw_hparams_t* hp, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* One tensor of dm_grad_clip.  `out` (NULL: not written) gets the clipped
+ * gradient; it may be `grad` itself when the types are the same. */
+typedef struct {
+  int64_t numel;
+  const void* grad;
+  void* out;
+  int32_t grad_dtype;
+  int32_t out_dtype;    /* ignored without out */
+} dm_grad_t;
+
+/* Bytes of device workspace dm_grad_clip needs (256-byte aligned, no
+ * initialisation).  Host-only. */
+dm_status_t dm_grad_clip_workspace_size(const dm_grad_t* tensors, int n, size_t* bytes);
+
+/* The Euclidean norm over all tensors together, and clipping by it:
+ *   result[0] = sqrt(sum grad^2)
+ *   result[1] = min(1, max_norm / result[0])   (1 for a zero norm)
+ *   out       = grad * result[1], rounded to nearest even
+ * `result` is a DEVICE float[2]; max_norm > 0 (INFINITY: the norm only, out
+ * is a copy).  The sum is taken in a fixed order (the same inputs give the
+ * same bits), with squares that leave fp32's range taken in fp64.
+ * Where the norm is not finite in fp32, result[0] holds it (inf or NaN), result[1]
+ * is NaN, no `out` is written and the device status reads DM_ERR_NONFINITE;
+ * dm_adamw_step given that result[1] as grad_scale skips its step.
+ * An `out` that is `grad` itself is not rewritten when result[1] = 1.
+ * Asynchronous on `stream`. */
+dm_status_t dm_grad_clip(const dm_grad_t* tensors, int n, float max_norm,
+                         float* result, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* dm_status_string(int32_t status);
 

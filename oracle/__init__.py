@@ -10,3 +10,4 @@ from .dimuon_oracle import (  # noqa: F401
     optimizer_step, polar_factor_svd, round_bf16, scale_factor, store_round,
     top_column_share, vector_matrix_shape, vector_step, vector_to_matrix, matrix_to_vector,
 )
+from . import adamw_oracle  # noqa: F401
