@@ -18,6 +18,9 @@ namespace {
 constexpr size_t HEADER_BYTES = 1024;      // status word at 0, AdamwScalars at 64
 constexpr size_t SCALARS_OFFSET = 64;
 constexpr int64_t MAX_NUMEL = int64_t(1) << 40;
+// From this many elements on, a CTA takes four passes of one tensor (there are
+// then seven CTAs and more for each SM).
+constexpr int64_t ADAMW8_LONG = int64_t(1) << 24;
 constexpr int64_t MAX_TILES = (int64_t(1) << 31) - 1;  // CTAs of one launch
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -223,32 +226,42 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
         });
     if (st != DM_OK) return st;
   }
-  if (!order[DM_STATE_8BIT].empty()) {
-    static thread_local Adamw8Params<MANY_SMALL> small;
-    static thread_local Adamw8Params<MANY_MAX> large;
-    st = in_launches(
-        order[DM_STATE_8BIT], small, large,
-        [&](int i) { return tile_count(ts[i].numel, 0, ADAMW8_TILE); },
-        [&](auto& p, int q, int i) {
-          const dm_adamw_tensor_t& t = ts[i];
-          p.W[q] = t.weight;
-          p.G[q] = t.grad;
-          p.M[q] = t.moment1;
-          p.V[q] = t.moment2;
-          p.S1[q] = t.scale1;
-          p.S2[q] = t.scale2;
-          p.n_flags[q] = t.numel << 8 | adamw_flags(t);
-          p.lr_mult[q] = t.lr_mult;
-          p.decay_mult[q] = t.decay_mult;
-          p.index[q] = (uint32_t)i;
-        },
-        [&](auto& p, int count, int tiles) {
-          p.h = h;
-          p.h.count = count;
-          return launch_adamw8(p, tiles, s);
-        });
-    if (st != DM_OK) return st;
-  }
+  for (int wdt = DM_BF16; wdt <= DM_FP32; ++wdt)
+    for (int gdt = DM_BF16; gdt <= DM_FP32; ++gdt) {
+      std::vector<int> list;  // one launch takes tensors of the same types
+      int64_t elems = 0;
+      for (int i : order[DM_STATE_8BIT])
+        if (ts[i].weight_dtype == wdt && ts[i].grad_dtype == gdt) {
+          list.push_back(i);
+          elems += ts[i].numel;
+        }
+      if (list.empty()) continue;
+      const int tile = elems >= ADAMW8_LONG ? 4 * ADAMW8_PASS : ADAMW8_PASS;
+      static thread_local Adamw8Params<MANY_SMALL> small;
+      static thread_local Adamw8Params<MANY_MAX> large;
+      st = in_launches(
+          list, small, large, [&](int i) { return tile_count(ts[i].numel, 0, tile); },
+          [&](auto& p, int q, int i) {
+            const dm_adamw_tensor_t& t = ts[i];
+            p.W[q] = t.weight;
+            p.G[q] = t.grad;
+            p.M[q] = t.moment1;
+            p.V[q] = t.moment2;
+            p.S1[q] = t.scale1;
+            p.S2[q] = t.scale2;
+            p.n_flags[q] = t.numel << 8 | adamw_flags(t);
+            p.lr_mult[q] = t.lr_mult;
+            p.decay_mult[q] = t.decay_mult;
+            p.index[q] = (uint32_t)i;
+          },
+          [&](auto& p, int count, int tiles) {
+            p.h = h;
+            p.h.count = count;
+            p.tile_elems = tile;
+            return launch_adamw8(p, wdt, gdt, tiles, s);
+          });
+      if (st != DM_OK) return st;
+    }
   return DM_OK;
 }
 

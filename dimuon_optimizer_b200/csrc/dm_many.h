@@ -24,7 +24,8 @@ enum {
 
 // ------------------------------- AdamW ------------------------------------
 constexpr int ADAMW32_TILE = 2048;  // elements per CTA pass, 8 per thread
-constexpr int ADAMW8_TILE = 4096;   // 16 per thread: 8 threads share a block's scale
+constexpr int ADAMW8_PASS = 4096;   // elements a CTA takes at a time, 16 per thread: 8 threads
+                                    // share a block's scale
 
 // Values that depend on the step, computed on the host, or by adamw_scalars
 // when the step is counted on the device.
@@ -62,6 +63,7 @@ struct Adamw32Params {
 template <int N>
 struct Adamw8Params {
   AdamwHead h;
+  int tile_elems;            // elements per CTA, a multiple of ADAMW8_PASS
   void* W[N];
   const void* G[N];
   void* M[N];
@@ -89,7 +91,7 @@ struct AdamwScalarsParams {
 template <int N>
 cudaError_t launch_adamw32(const Adamw32Params<N>& p, int tiles, cudaStream_t s);
 template <int N>
-cudaError_t launch_adamw8(const Adamw8Params<N>& p, int tiles, cudaStream_t s);
+cudaError_t launch_adamw8(const Adamw8Params<N>& p, int wdt, int gdt, int grid, cudaStream_t s);
 cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s);
 
 // The 32-bit mixing step of the rounding's hash (host and device): two

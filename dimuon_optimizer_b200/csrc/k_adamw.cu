@@ -6,6 +6,7 @@
 // per element with fp32 moments, 10.1 with 8-bit ones), so HBM bounds it.
 #include <cuda_fp8.h>
 
+#include "dimuon.h"
 #include "dm_common.cuh"
 #include "dm_many.h"
 
@@ -23,24 +24,23 @@ struct Coef {
   float gs;            // gradient scale
   float b1, c1, b2, c2, eps;
   float isb2;          // 1 / sqrt(1 - b2^t)
-  float step;          // lr / (1 - b1^t)
-  float decay;         // 1 - lr wd
+  float inv_bc1;       // 1 / (1 - b1^t)
+  float lr, wd;        // without the tensor's multipliers
   uint32_t step_key;
   bool skip;
 };
 
 // Reads the step's device values; the status word is written by one thread
 // of a host-counted step (adamw_scalars has written it otherwise).
-__device__ __forceinline__ Coef coefficients(const AdamwHead& h, float lr_mult, float decay_mult) {
+__device__ __forceinline__ Coef coefficients(const AdamwHead& h) {
   Coef c;
   c.gs = h.grad_scale ? *h.grad_scale : 1.f;
-  const float lr0 = h.lr_dev ? *h.lr_dev : h.lr;
+  c.lr = h.lr_dev ? *h.lr_dev : h.lr;
   const AdamwScalars sc = h.dev ? *h.dev : h.sc;
-  c.skip = h.dev ? sc.skip != 0 : !(finite_f(c.gs) && finite_f(lr0));
+  c.skip = h.dev ? sc.skip != 0 : !(finite_f(c.gs) && finite_f(c.lr));
   c.b1 = h.b1; c.c1 = h.c1; c.b2 = h.b2; c.c2 = h.c2; c.eps = h.eps;
-  const float lr = lr0 * lr_mult;
-  c.step = lr * sc.inv_bc1;
-  c.decay = fmaf(-lr, h.wd * decay_mult, 1.f);
+  c.wd = h.wd;
+  c.inv_bc1 = sc.inv_bc1;
   c.isb2 = sc.inv_sqrt_bc2;
   c.step_key = sc.step_key;
   if (h.write_status && blockIdx.x == 0 && threadIdx.x == 0)
@@ -59,11 +59,12 @@ __device__ __forceinline__ void moments(const Coef& c, float g, float& m, float&
 
 // The new weight; square root and division are the approximate ones (2 ulp:
 // they touch the update only, which is lr / |W| of the weight).
-__device__ __forceinline__ float updated(const Coef& c, float w, float m, float v) {
+__device__ __forceinline__ float updated(const Coef& c, float step, float decay, float w, float m,
+                                         float v) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
   const float d = fmaf(r, c.isb2, c.eps);
-  return fmaf(w, c.decay, -c.step * __fdividef(m, d));
+  return fmaf(w, decay, -step * __fdividef(m, d));
 }
 
 // ---------------------------------------------------------------------------
@@ -72,10 +73,11 @@ __device__ __forceinline__ float updated(const Coef& c, float w, float m, float 
 // 32-byte aligned in fp32 (16 in bf16) whatever the tensor's offset.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void adamw32_elem(void* W, const void* G, float* M, float* V, int wdt,
-                                             int gdt, int64_t e, const Coef& c) {
+                                             int gdt, int64_t e, const Coef& c, float step,
+                                              float decay) {
   float m = M[e], v = V[e];
   moments(c, ld_elem(G, e, gdt), m, v);
-  const float w = updated(c, ld_elem(W, e, wdt), m, v);
+  const float w = updated(c, step, decay, ld_elem(W, e, wdt), m, v);
   M[e] = m;
   V[e] = v;
   st_elem(W, e, wdt, w);
@@ -85,8 +87,10 @@ template <int N>
 __global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ Adamw32Params<N> p) {
   const int tile = blockIdx.x;
   const int t = find_group(p.starts, p.h.count, tile);
-  const Coef c = coefficients(p.h, p.lr_mult[t], p.decay_mult[t]);
+  const Coef c = coefficients(p.h);
   if (c.skip) return;
+  const float lr = c.lr * p.lr_mult[t];
+  const float step = lr * c.inv_bc1, decay = fmaf(-lr, c.wd * p.decay_mult[t], 1.f);
   const int flags = p.flags[t];
   const int wdt = flags & MF_W_FP32 ? DT_FP32 : DT_BF16, gdt = flags & MF_G_FP32 ? DT_FP32 : DT_BF16;
   const int64_t n = p.n[t];
@@ -98,14 +102,14 @@ __global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ 
   if (!(flags & MF_VEC)) {
     for (int q = 0; q < 8; ++q) {
       const int64_t e = base + q * THREADS + threadIdx.x;
-      if (e < n) adamw32_elem(W, G, M, V, wdt, gdt, e, c);
+      if (e < n) adamw32_elem(W, G, M, V, wdt, gdt, e, c, step, decay);
     }
     return;
   }
   const int64_t e = base + threadIdx.x * 8 - ((flags >> MF_SHIFT_BIT) & 7);
   if (e < 0 || e + 8 > n) {
     for (int q = 0; q < 8; ++q)
-      if (e + q >= 0 && e + q < n) adamw32_elem(W, G, M, V, wdt, gdt, e + q, c);
+      if (e + q >= 0 && e + q < n) adamw32_elem(W, G, M, V, wdt, gdt, e + q, c, step, decay);
     return;
   }
   float g[8], m[8], v[8], w[8];
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ 
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     moments(c, g[q], m[q], v[q]);
-    w[q] = updated(c, w[q], m[q], v[q]);
+    w[q] = updated(c, step, decay, w[q], m[q], v[q]);
   }
   st8(M, e, DT_FP32, m);
   st8(V, e, DT_FP32, v);
@@ -124,9 +128,67 @@ __global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------------------
-// 8-bit moments.  A thread takes 16 consecutive elements, so 8 threads of a
-// warp share the scale of a block of 128.
+// 8-bit moments.  A thread takes 16 consecutive elements at a time, so 8
+// threads of a warp share the scale of a block of 128.
 // ---------------------------------------------------------------------------
+// Two fp32 numbers in one 64-bit register pair, for the packed fp32
+// instructions: half the issue slots of the separate ones, the same rounding.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ float2 split(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// Largest of |a|, |b|, |c|; NaN if any is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float sqrt_ftz(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Rounding to codes.  x in units of its code's format, multiplied by 2^-120
+// (e4m3) or 2^-112 (e5m2), lies where the fp32 exponent field counts like the
+// code's: the code's bits then stand in the fp32 pattern 20 (21) places up, the
+// subnormal codes as fp32 subnormals, and the bits below are the remainder.
+// Adding noise to them and cutting them off takes the upper neighbour with the
+// remainder's probability.
+// Two factors, as their product leaves fp32 for large scales.
+constexpr float E4M3_TO_BITS = 7.52316384526264e-37f;   // 2^-120
+constexpr float E5M2_TO_BITS = 1.925929944387236e-34f;  // 2^-112
+
 // Smallest power of two s >= 2^-110 with the magnitude of `bits` <= 1.75 2^top s,
 // and its inverse; NaN for a non-finite magnitude.
 __device__ __forceinline__ void block_scale(uint32_t bits, int top, float& s, float& inv) {
@@ -135,128 +197,225 @@ __device__ __forceinline__ void block_scale(uint32_t bits, int top, float& s, fl
   inv = __uint_as_float((uint32_t)(254 - e) << 23);
 }
 
-// Code of x >= 0 (x at most the format's largest value) with MAN mantissa bits
-// and exponent bias BIAS.  The bits of an fp32 number below the code's last
-// place are its remainder, so adding noise there and cutting off rounds up
-// with the remainder's probability.  Below the least normal number L, x + L
-// lies on the spacing of the subnormal codes.
-template <int MAN, int BIAS>
-__device__ __forceinline__ uint32_t encode(float x, uint32_t noise) {
-  constexpr float L = BIAS == 7 ? 0.015625f : 6.103515625e-05f;  // 2^(1 - BIAS)
-  const bool small = x < L;
-  const float y = small ? x + L : x;
-  const uint32_t off = (uint32_t)((127 - BIAS) << MAN) + (small ? (1u << MAN) : 0u);
-  return ((__float_as_uint(y) + noise) >> (23 - MAN)) - off;
-}
-
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {  // over 8 neighbouring lanes
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
-template <int N>
-__global__ void __launch_bounds__(THREADS) adamw8_step(const __grid_constant__ Adamw8Params<N> p) {
+template <int DT>
+__device__ __forceinline__ void* elem_ptr(const void* p, int64_t e) {
+  return const_cast<char*>(reinterpret_cast<const char*>(p)) + e * (DT == DT_BF16 ? 2 : 4);
+}
+
+// 16 elements of a buffer as they lie in memory: `cnt` of them from element
+// e on, zero bits behind; `vec`: all 16, on a 16-byte boundary.
+template <int DT>
+struct Raw16 {
+  static constexpr int WORDS = DT == DT_BF16 ? 8 : 16;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const void* p, uint32_t e, int cnt, bool vec) {
+    if (vec) {
+      const uint4* q = reinterpret_cast<const uint4*>(elem_ptr<DT>(p, e));
+#pragma unroll
+      for (int i = 0; i < WORDS / 4; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = q[i];
+    } else if (DT == DT_BF16) {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + e;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = (2 * i < cnt ? (uint32_t)q[2 * i] : 0u) |
+               (2 * i + 1 < cnt ? (uint32_t)q[2 * i + 1] << 16 : 0u);
+    } else {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + e;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i % WORDS] = i < cnt ? q[i] : 0u;
+    }
+  }
+  __device__ __forceinline__ F2 pair(int q) const {  // elements 2q, 2q + 1
+    if (DT == DT_BF16)
+      return f2(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xffff0000u));
+    return f2(__uint_as_float(w[(2 * q) % WORDS]), __uint_as_float(w[(2 * q + 1) % WORDS]));
+  }
+  __device__ __forceinline__ void set(int q, F2 x) {
+    const float2 f = split(x);
+    if (DT == DT_BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+      w[q] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      w[(2 * q) % WORDS] = __float_as_uint(f.x);
+      w[(2 * q + 1) % WORDS] = __float_as_uint(f.y);
+    }
+  }
+  __device__ __forceinline__ void store(void* p, uint32_t e, int cnt, bool vec) const {
+    if (vec) {
+      uint4* q = reinterpret_cast<uint4*>(elem_ptr<DT>(p, e));
+#pragma unroll
+      for (int i = 0; i < WORDS / 4; ++i) q[i] = *reinterpret_cast<const uint4*>(w + 4 * i);
+    } else if (DT == DT_BF16) {
+      uint16_t* q = reinterpret_cast<uint16_t*>(p) + e;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < cnt) q[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+    } else {
+      uint32_t* q = reinterpret_cast<uint32_t*>(p) + e;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < cnt) q[i] = w[i % WORDS];
+    }
+  }
+};
+
+// 16 codes, four to a word.
+struct Codes16 {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const void* p8, uint32_t e, int cnt, bool vec) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(p8) + e;
+    if (vec) {
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i % 4 == 0) w[i / 4] = 0;
+        if (i < cnt) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void* p8, uint32_t e, int cnt, bool vec) const {
+    uint8_t* p = reinterpret_cast<uint8_t*>(p8) + e;
+    if (vec) {
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < cnt) p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+  }
+  __device__ __forceinline__ F2 pair(int q, __nv_fp8_interpretation_t kind) const {
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(w[q / 2] >> (16 * (q % 2))), kind)));
+    return f2(f.x, f.y);
+  }
+  // Byte 3 of the four words.
+  __device__ __forceinline__ void gather(int i, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    w[i] = __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+  }
+};
+
+// Bound by HBM up to the power limit: 262 M elements (bf16 weights and
+// gradients) take 400 us (6.66 TB/s) while the clock stays at 1.96 GHz, 449 us
+// (0.90 of the measured copy) in a long run, when the part reaches its 1000 W
+// and the clock falls to 1.6 GHz: 40 instructions per element then fill three
+// quarters of the issue slots.  The first form (one fp32 operation at a time,
+// separate code for the subnormal codes, one pass per CTA) took 88 instructions
+// and 837 us.  Packed fp32 arithmetic, the codes' bits by a power-of-two
+// product, the packed fp8 conversions and the test for zero codes four at a
+// time brought that down.  A CTA takes four passes, so that finding its tensor
+// and the coefficients costs little (2 passes: 466 us; 8: 444 us, but 152
+// instead of 142 us on 448 tensors of 131072 elements).  Reading the next pass
+// into registers during this one made it twice as slow (128 registers).
+// Registers are held to 64, four CTAs per SM (without the limit 66 to 104 by
+// type: 458 us, and 182 instead of 173 us with 66 M fp32 weights and gradients).
+template <int N, int WDT, int GDT>
+__global__ void __launch_bounds__(THREADS, 4)
+    adamw8_step(const __grid_constant__ Adamw8Params<N> p) {
   const int tile = blockIdx.x;
   const int t = find_group(p.starts, p.h.count, tile);
-  const Coef c = coefficients(p.h, p.lr_mult[t], p.decay_mult[t]);
+  const Coef c = coefficients(p.h);
   if (c.skip) return;
-  const int flags = (int)(p.n_flags[t] & 0xff);
   const int64_t n = p.n_flags[t] >> 8;
-  const int wdt = flags & MF_W_FP32 ? DT_FP32 : DT_BF16, gdt = flags & MF_G_FP32 ? DT_FP32 : DT_BF16;
-  void* W = p.W[t];
-  const void* G = p.G[t];
-  uint8_t* M = reinterpret_cast<uint8_t*>(p.M[t]);
-  uint8_t* V = reinterpret_cast<uint8_t*>(p.V[t]);
-  const int64_t e = (int64_t)(tile - p.starts[t]) * ADAMW8_TILE + threadIdx.x * 16;
-  const int64_t blk = e / 128;
-  const bool full = (flags & MF_VEC) && e + 16 <= n;
-  const int cnt = e >= n ? 0 : (int)min((int64_t)16, n - e);
+  const int64_t first = (int64_t)(tile - p.starts[t]) * p.tile_elems;  // of this CTA
+  const bool aligned = (p.n_flags[t] & MF_VEC) != 0;
+  const int left = (int)min(n - first, (int64_t)p.tile_elems);  // elements of this CTA
+  const void* G = elem_ptr<GDT>(p.G[t], first);
+  void* W = elem_ptr<WDT>(p.W[t], first);
+  uint8_t* M = reinterpret_cast<uint8_t*>(p.M[t]) + first;
+  uint8_t* V = reinterpret_cast<uint8_t*>(p.V[t]) + first;
+  float* S1 = p.S1[t] + first / DM_ADAMW_BLOCK;
+  float* S2 = p.S2[t] + first / DM_ADAMW_BLOCK;
+  const uint64_t group = (uint64_t)first >> 4;  // 2^32 groups are whole tiles: one upper half
+  const uint32_t key =
+      many_mix(many_mix(c.step_key + p.index[t]) + (uint32_t)(group >> 32)) ^ (uint32_t)group;
+  const float lr = c.lr * p.lr_mult[t];
+  const F2 gs = f2(c.gs), c1 = f2(c.c1), c2 = f2(c.c2), isb2 = f2(c.isb2), eps = f2(c.eps),
+           nstep = f2(-(lr * c.inv_bc1)), decay = f2(fmaf(-lr, c.wd * p.decay_mult[t], 1.f));
 
-  float g[16], w[16], m[16], v[16];
-  uint32_t cm[4] = {0, 0, 0, 0}, cv[4] = {0, 0, 0, 0};
-  float s1 = 0.f, s2 = 0.f;
-  if (cnt) {
-    s1 = p.S1[t][blk];
-    s2 = p.S2[t][blk];
-  }
-  if (full) {
-    *reinterpret_cast<uint4*>(cm) = *reinterpret_cast<const uint4*>(M + e);
-    *reinterpret_cast<uint4*>(cv) = *reinterpret_cast<const uint4*>(V + e);
-    ld8(G, e, gdt, g);
-    ld8(G, e + 8, gdt, g + 8);
-    ld8(W, e, wdt, w);
-    ld8(W, e + 8, wdt, w + 8);
-  } else {
+  for (uint32_t e = threadIdx.x * 16; e - threadIdx.x * 16 < (uint32_t)left; e += ADAMW8_PASS) {
+    const int cnt = min(max(left - (int)e, 0), 16);
+    const bool vec = aligned && cnt == 16;
+    const uint32_t blk = e / DM_ADAMW_BLOCK;
+    Raw16<GDT> g;
+    Raw16<WDT> w;
+    Codes16 cm, cv;
+    g.load(G, e, cnt, vec);
+    w.load(W, e, cnt, vec);
+    cm.load(M, e, cnt, vec);
+    cv.load(V, e, cnt, vec);
+    float s1 = 0.f, s2 = 0.f;
+    if (cnt) {
+      s1 = S1[blk];
+      s2 = S2[blk];
+    }
+    // code x scale x beta: the scale is a power of two, so scale x beta is exact and the product
+    // is rounded once, as code x scale (exact) times beta
+    const F2 sb1 = f2(s1 * c.b1), sb2 = f2(s2 * c.b2);
+    F2 m[8], v[8];
+    float top1 = 0.f, top2 = 0.f;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      g[q] = w[q] = 0.f;
-      if (q < cnt) {
-        cm[q / 4] |= (uint32_t)M[e + q] << (8 * (q % 4));
-        cv[q / 4] |= (uint32_t)V[e + q] << (8 * (q % 4));
-        g[q] = ld_elem(G, e + q, gdt);
-        w[q] = ld_elem(W, e + q, wdt);
+    for (int q = 0; q < 8; ++q) {
+      // products and sums rounded one by one: the rounding below compares these bits with its
+      // noise, so their value is part of the operator's definition
+      const F2 gq = mul2(g.pair(q), gs);
+      m[q] = add2(mul2(cm.pair(q, __NV_E4M3), sb1), mul2(gq, c1));
+      v[q] = add2(mul2(cv.pair(q, __NV_E5M2), sb2), mul2(mul2(gq, gq), c2));
+      const float2 mf = split(m[q]), vf = split(v[q]);
+      top1 = max3_abs(top1, mf.x, mf.y);
+      top2 = max3_abs(top2, vf.x, vf.y);
+      const float2 d = split(fma2(f2(sqrt_ftz(vf.x), sqrt_ftz(vf.y)), isb2, eps));
+      w.set(q, fma2(mul2(m[q], nstep), f2(rcp_ftz(d.x), rcp_ftz(d.y)), mul2(w.pair(q), decay)));
+    }
+    w.store(W, e, cnt, vec);
+    float i1, i2;
+    block_scale(group_max(__float_as_uint(top1)), 8, s1, i1);
+    block_scale(group_max(__float_as_uint(top2)), 15, s2, i2);
+    const uint32_t h0 = many_mix(key ^ e / 16) * 0x7FEB352Du;
+    uint32_t zero = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = 4 * k + j;
+        const float2 xm = split(mul2(mul2(m[q / 2], f2(i1)), f2(E4M3_TO_BITS)));
+        const float2 xv = split(mul2(mul2(v[q / 2], f2(i2)), f2(E5M2_TO_BITS)));
+        uint32_t h = h0 + (uint32_t)q * (MANY_GOLDEN * 0x7FEB352Du);
+        h = (h ^ (h >> 15)) * 0x846CA68Bu;
+        // the hash's last round, h ^= h >> 16, leaves the upper half: noise of the first moment
+        // from the upper half, of the second from the lower, each moved to bits 8-23 (16 bits
+        // below the code in byte 3)
+        const uint32_t n1 = __byte_perm(h, 0, 0x4324), n2 = __byte_perm(h, 0, 0x4104) ^ n1;
+        const uint32_t bm = __float_as_uint(q & 1 ? xm.y : xm.x);  // sign, 7 code bits from 20 on
+        const uint32_t bv = __float_as_uint(q & 1 ? xv.y : xv.x);  // 8 code bits from 21 on
+        a[j] = ((bm << 4) + n1) | (bm & 0x80000000u);
+        b[j] = (bv << 3) + n2;
+      }
+      cm.gather(k, a[0], a[1], a[2], a[3]);
+      cv.gather(k, b[0], b[1], b[2], b[3]);
+      zero |= (cv.w[k] - 0x01010101u) & ~cv.w[k] & 0x80808080u;
+    }
+    if (zero) {  // a zero code: a positive second moment takes the least positive one
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const float2 f = split(v[q / 2]);
+        if ((q & 1 ? f.y : f.x) > 0.f && (cv.w[q / 4] >> (8 * (q % 4)) & 0xffu) == 0)
+          cv.w[q / 4] |= 1u << (8 * (q % 4));
       }
     }
-  }
-  uint32_t top1 = 0, top2 = 0;
-#pragma unroll
-  for (int q = 0; q < 16; q += 2) {
-    const uint32_t a = cm[q / 4] >> (8 * (q % 4)), b = cv[q / 4] >> (8 * (q % 4));
-    const float2 fm = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)a, __NV_E4M3)));
-    const float2 fv = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)b, __NV_E5M2)));
-    m[q] = fm.x * s1;
-    m[q + 1] = fm.y * s1;
-    v[q] = fv.x * s2;
-    v[q + 1] = fv.y * s2;
-#pragma unroll
-    for (int i = q; i < q + 2; ++i) {
-      if (i >= cnt) { m[i] = v[i] = 0.f; }  // behind the tensor's end (g = 0 there)
-      moments(c, g[i], m[i], v[i]);
-      w[i] = updated(c, w[i], m[i], v[i]);
-      top1 = max(top1, __float_as_uint(m[i]) & 0x7fffffffu);
-      top2 = max(top2, __float_as_uint(v[i]) & 0x7fffffffu);
+    cm.store(M, e, cnt, vec);
+    cv.store(V, e, cnt, vec);
+    if (cnt && (threadIdx.x & 7) == 0) {
+      S1[blk] = s1;
+      S2[blk] = s2;
     }
-  }
-  top1 = group_max(top1);
-  top2 = group_max(top2);
-  float i1, i2;
-  block_scale(top1, 8, s1, i1);
-  block_scale(top2, 15, s2, i2);
-  const uint64_t group = (uint64_t)e >> 4;
-  const uint32_t key = many_mix(many_mix(c.step_key + p.index[t]) + (uint32_t)(group >> 32));
-  const uint32_t h0 = many_mix(key ^ (uint32_t)group);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) cm[q] = cv[q] = 0;
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    uint32_t h = (h0 + (uint32_t)q * MANY_GOLDEN) * 0x7FEB352Du;
-    h = (h ^ (h >> 15)) * 0x846CA68Bu;
-    h ^= h >> 16;
-    const uint32_t a = encode<3, 7>(fabsf(m[q]) * i1, (h >> 16) << 4) |
-                       (__float_as_uint(m[q]) >> 31 << 7);
-    uint32_t b = encode<2, 15>(v[q] * i2, (h & 0xffffu) << 5);
-    if (v[q] > 0.f && b == 0) b = 1;
-    cm[q / 4] |= (a & 0xffu) << (8 * (q % 4));
-    cv[q / 4] |= (b & 0xffu) << (8 * (q % 4));
-  }
-  if (full) {
-    *reinterpret_cast<uint4*>(M + e) = *reinterpret_cast<const uint4*>(cm);
-    *reinterpret_cast<uint4*>(V + e) = *reinterpret_cast<const uint4*>(cv);
-    st8(W, e, wdt, w);
-    st8(W, e + 8, wdt, w + 8);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 16; ++q)
-      if (q < cnt) {
-        M[e + q] = (uint8_t)(cm[q / 4] >> (8 * (q % 4)));
-        V[e + q] = (uint8_t)(cv[q / 4] >> (8 * (q % 4)));
-        st_elem(W, e + q, wdt, w[q]);
-      }
-  }
-  if (cnt && (threadIdx.x & 7) == 0) {
-    p.S1[t][blk] = s1;
-    p.S2[t][blk] = s2;
   }
 }
 
@@ -284,8 +443,15 @@ cudaError_t launch_adamw32(const Adamw32Params<N>& p, int tiles, cudaStream_t s)
   return cudaGetLastError();
 }
 template <int N>
-cudaError_t launch_adamw8(const Adamw8Params<N>& p, int tiles, cudaStream_t s) {
-  adamw8_step<N><<<tiles, THREADS, 0, s>>>(p);
+cudaError_t launch_adamw8(const Adamw8Params<N>& p, int wdt, int gdt, int grid, cudaStream_t s) {
+  if (wdt == DT_BF16 && gdt == DT_BF16)
+    adamw8_step<N, DT_BF16, DT_BF16><<<grid, THREADS, 0, s>>>(p);
+  else if (wdt == DT_BF16)
+    adamw8_step<N, DT_BF16, DT_FP32><<<grid, THREADS, 0, s>>>(p);
+  else if (gdt == DT_BF16)
+    adamw8_step<N, DT_FP32, DT_BF16><<<grid, THREADS, 0, s>>>(p);
+  else
+    adamw8_step<N, DT_FP32, DT_FP32><<<grid, THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s) {
@@ -294,7 +460,7 @@ cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s) {
 }
 template cudaError_t launch_adamw32(const Adamw32Params<MANY_SMALL>&, int, cudaStream_t);
 template cudaError_t launch_adamw32(const Adamw32Params<MANY_MAX>&, int, cudaStream_t);
-template cudaError_t launch_adamw8(const Adamw8Params<MANY_SMALL>&, int, cudaStream_t);
-template cudaError_t launch_adamw8(const Adamw8Params<MANY_MAX>&, int, cudaStream_t);
+template cudaError_t launch_adamw8(const Adamw8Params<MANY_SMALL>&, int, int, int, cudaStream_t);
+template cudaError_t launch_adamw8(const Adamw8Params<MANY_MAX>&, int, int, int, cudaStream_t);
 
 }  // namespace dm

@@ -164,6 +164,40 @@ def test_8bit_moments(wdt, gdt, shift):
             check_fp32(*h, hp, t, to_host(b[0].t), None, None, wdt, 0.5)
 
 
+def test_8bit_blocks_of_extreme_range():
+    """Blocks whose largest gradient is 1e18 .. 1e-19, with far smaller ones
+    beside it: codes and scales as the oracle's, positive second moments above zero."""
+    rng = np.random.default_rng(21)
+    tops = [1e18, 1e15, 1e12, 1e9, 1e6, 1.0, 1e-9, 1e-15, 1e-19]
+    G = []
+    for top in tops:
+        b = rng.standard_normal(128) * top * 10.0 ** -rng.uniform(0, 22, 128)
+        b[rng.integers(128)] = top
+        b[rng.integers(1, 128)] = 0.0
+        G.append(b)
+    G = np.concatenate(G).astype(np.float32)
+    W = torch.zeros(len(G), device="cuda")
+    g = torch.from_numpy(G).cuda()
+    st = dm.dm_adamw_state(W, dm.DM_STATE_8BIT)
+    hp = dm.dm_adamw_default_hparams(seed=2)
+    p = ao.AdamWParams(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay)
+    ts = [dm.dm_adamw_tensor(W, g, *st)]
+    ws = workspace(ts, hp)
+    z = np.zeros(len(G))
+    h = (z, z)
+    for t in (1, 2):
+        hp.step = t
+        dm.check(dm.dm_adamw_step(ts, hp, ws))
+        m32, v32 = ao.moments_f32(G, *h, p)
+        c1, s1, c2, s2 = ao.pack_moments(m32.astype(float), v32.astype(float), 2, t, 0)
+        np.testing.assert_array_equal(to_host(st[2]), s1)
+        np.testing.assert_array_equal(to_host(st[3]), s2)
+        np.testing.assert_array_equal(st[0].view(torch.uint8).cpu().numpy(), c1)
+        np.testing.assert_array_equal(st[1].view(torch.uint8).cpu().numpy(), c2)
+        assert ((c2 > 0) == (v32 > 0)).all()
+        h = (ao.unpack(c1, s1, ao.E4M3), ao.unpack(c2, s2, ao.E5M2))
+
+
 def test_many_tensors_and_both_states_in_one_call():
     """More tensors than one launch holds, the two state formats mixed; the
     8-bit noise goes by the position in the call."""
