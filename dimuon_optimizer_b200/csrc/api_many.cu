@@ -111,7 +111,8 @@ uint8_t adamw_flags(const dm_adamw_tensor_t& t) {
   int f = (t.weight_dtype == DM_FP32 ? MF_W_FP32 : 0) | (t.grad_dtype == DM_FP32 ? MF_G_FP32 : 0);
   const int s = offset8(t.weight, wsz);
   if (t.state == DM_STATE_8BIT) {
-    if (s == 0 && offset8(t.grad, gsz) == 0 && aligned(t.moment1, 16) && aligned(t.moment2, 16))
+    if (aligned(t.weight, 32) && aligned(t.grad, 32) && aligned(t.moment1, 16) &&
+        aligned(t.moment2, 16))
       f |= MF_VEC;
   } else if (offset8(t.grad, gsz) == s && offset8(t.moment1, 4) == s && offset8(t.moment2, 4) == s) {
     f |= MF_VEC | s << MF_SHIFT_BIT;
@@ -177,10 +178,8 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
   h.lr_dev = hp->lr_dev;
   h.grad_scale = hp->grad_scale;
   h.status = status;
-  std::vector<int> order[2];
-  for (int i = 0; i < n; ++i)
-    if (ts[i].numel > 0) order[ts[i].state].push_back(i);
-  const bool any = !order[0].empty() || !order[1].empty();
+  bool any = false;
+  for (int i = 0; i < n; ++i) any = any || ts[i].numel > 0;
   if (hp->step_counter) {
     AdamwScalarsParams sp;
     sp.counter = hp->step_counter;
@@ -202,65 +201,67 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
     if (!any) DM_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
   }
 
-  if (!order[DM_STATE_FP32].empty()) {
-    static thread_local Adamw32Params<MANY_SMALL> small;
-    static thread_local Adamw32Params<MANY_MAX> large;
-    st = in_launches(
-        order[DM_STATE_FP32], small, large,
-        [&](int i) { return tile_count(ts[i].numel, adamw_flags(ts[i]), ADAMW32_TILE); },
-        [&](auto& p, int q, int i) {
-          const dm_adamw_tensor_t& t = ts[i];
-          p.W[q] = t.weight;
-          p.G[q] = t.grad;
-          p.M[q] = reinterpret_cast<float*>(t.moment1);
-          p.V[q] = reinterpret_cast<float*>(t.moment2);
-          p.n[q] = t.numel;
-          p.lr_mult[q] = t.lr_mult;
-          p.decay_mult[q] = t.decay_mult;
-          p.flags[q] = adamw_flags(t);
-        },
-        [&](auto& p, int count, int tiles) {
-          p.h = h;
-          p.h.count = count;
-          return launch_adamw32(p, tiles, s);
-        });
-    if (st != DM_OK) return st;
-  }
+  // one launch takes tensors of the same state format and types
   for (int wdt = DM_BF16; wdt <= DM_FP32; ++wdt)
     for (int gdt = DM_BF16; gdt <= DM_FP32; ++gdt) {
-      std::vector<int> list;  // one launch takes tensors of the same types
-      int64_t elems = 0;
-      for (int i : order[DM_STATE_8BIT])
-        if (ts[i].weight_dtype == wdt && ts[i].grad_dtype == gdt) {
-          list.push_back(i);
-          elems += ts[i].numel;
-        }
-      if (list.empty()) continue;
-      const int tile = elems >= ADAMW8_LONG ? 4 * ADAMW8_PASS : ADAMW8_PASS;
-      static thread_local Adamw8Params<MANY_SMALL> small;
-      static thread_local Adamw8Params<MANY_MAX> large;
-      st = in_launches(
-          list, small, large, [&](int i) { return tile_count(ts[i].numel, 0, tile); },
-          [&](auto& p, int q, int i) {
-            const dm_adamw_tensor_t& t = ts[i];
-            p.W[q] = t.weight;
-            p.G[q] = t.grad;
-            p.M[q] = t.moment1;
-            p.V[q] = t.moment2;
-            p.S1[q] = t.scale1;
-            p.S2[q] = t.scale2;
-            p.n_flags[q] = t.numel << 8 | adamw_flags(t);
-            p.lr_mult[q] = t.lr_mult;
-            p.decay_mult[q] = t.decay_mult;
-            p.index[q] = (uint32_t)i;
-          },
-          [&](auto& p, int count, int tiles) {
-            p.h = h;
-            p.h.count = count;
-            p.tile_elems = tile;
-            return launch_adamw8(p, wdt, gdt, tiles, s);
-          });
-      if (st != DM_OK) return st;
+      std::vector<int> fp32, eight;
+      int64_t elems8 = 0;
+      for (int i = 0; i < n; ++i) {
+        if (ts[i].numel == 0 || ts[i].weight_dtype != wdt || ts[i].grad_dtype != gdt) continue;
+        const bool is8 = ts[i].state == DM_STATE_8BIT;
+        (is8 ? eight : fp32).push_back(i);
+        if (is8) elems8 += ts[i].numel;
+      }
+      auto common = [&](auto& p, int q, int i) {
+        const dm_adamw_tensor_t& t = ts[i];
+        p.W[q] = t.weight;
+        p.G[q] = t.grad;
+        p.lr_mult[q] = t.lr_mult;
+        p.decay_mult[q] = t.decay_mult;
+      };
+      if (!fp32.empty()) {
+        static thread_local Adamw32Params<MANY_SMALL> small;
+        static thread_local Adamw32Params<MANY_MAX> large;
+        st = in_launches(
+            fp32, small, large,
+            [&](int i) { return tile_count(ts[i].numel, adamw_flags(ts[i]), ADAMW32_TILE); },
+            [&](auto& p, int q, int i) {
+              common(p, q, i);
+              p.M[q] = reinterpret_cast<float*>(ts[i].moment1);
+              p.V[q] = reinterpret_cast<float*>(ts[i].moment2);
+              p.n[q] = ts[i].numel;
+              p.flags[q] = adamw_flags(ts[i]);
+            },
+            [&](auto& p, int count, int tiles) {
+              p.h = h;
+              p.h.count = count;
+              return launch_adamw32(p, wdt, gdt, tiles, s);
+            });
+        if (st != DM_OK) return st;
+      }
+      if (!eight.empty()) {
+        static thread_local Adamw8Params<MANY_SMALL> small;
+        static thread_local Adamw8Params<MANY_MAX> large;
+        const int tile = elems8 >= ADAMW8_LONG ? 4 * ADAMW8_PASS : ADAMW8_PASS;
+        st = in_launches(
+            eight, small, large, [&](int i) { return tile_count(ts[i].numel, 0, tile); },
+            [&](auto& p, int q, int i) {
+              common(p, q, i);
+              p.M[q] = ts[i].moment1;
+              p.V[q] = ts[i].moment2;
+              p.S1[q] = ts[i].scale1;
+              p.S2[q] = ts[i].scale2;
+              p.n_flags[q] = ts[i].numel << 8 | adamw_flags(ts[i]);
+              p.index[q] = (uint32_t)i;
+            },
+            [&](auto& p, int count, int tiles) {
+              p.h = h;
+              p.h.count = count;
+              p.tile_elems = tile;
+              return launch_adamw8(p, wdt, gdt, tiles, s);
+            });
+        if (st != DM_OK) return st;
+      }
     }
   return DM_OK;
 }

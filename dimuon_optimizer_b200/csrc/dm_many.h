@@ -23,7 +23,7 @@ enum {
 };
 
 // ------------------------------- AdamW ------------------------------------
-constexpr int ADAMW32_TILE = 2048;  // elements per CTA pass, 8 per thread
+constexpr int ADAMW32_TILE = 2048;  // elements per CTA, 8 per thread
 constexpr int ADAMW8_PASS = 4096;   // elements a CTA takes at a time, 16 per thread: 8 threads
                                     // share a block's scale
 
@@ -89,7 +89,7 @@ struct AdamwScalarsParams {
 };
 
 template <int N>
-cudaError_t launch_adamw32(const Adamw32Params<N>& p, int tiles, cudaStream_t s);
+cudaError_t launch_adamw32(const Adamw32Params<N>& p, int wdt, int gdt, int grid, cudaStream_t s);
 template <int N>
 cudaError_t launch_adamw8(const Adamw8Params<N>& p, int wdt, int gdt, int grid, cudaStream_t s);
 cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s);

@@ -48,89 +48,6 @@ __device__ __forceinline__ Coef coefficients(const AdamwHead& h) {
   return c;
 }
 
-// The moments, each product and sum rounded to fp32 by itself: the
-// stochastic rounding of the 8-bit form compares these bits with its noise,
-// so their value is part of the operator's definition.
-__device__ __forceinline__ void moments(const Coef& c, float g, float& m, float& v) {
-  g = __fmul_rn(g, c.gs);
-  m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.c1));
-  v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.c2));
-}
-
-// The new weight; square root and division are the approximate ones (2 ulp:
-// they touch the update only, which is lr / |W| of the weight).
-__device__ __forceinline__ float updated(const Coef& c, float step, float decay, float w, float m,
-                                         float v) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-  const float d = fmaf(r, c.isb2, c.eps);
-  return fmaf(w, decay, -step * __fdividef(m, d));
-}
-
-// ---------------------------------------------------------------------------
-// fp32 moments.  A thread takes 8 consecutive elements; group k of a tensor
-// covers elements 8k - shift .. 8k - shift + 7, so that whole groups are
-// 32-byte aligned in fp32 (16 in bf16) whatever the tensor's offset.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void adamw32_elem(void* W, const void* G, float* M, float* V, int wdt,
-                                             int gdt, int64_t e, const Coef& c, float step,
-                                              float decay) {
-  float m = M[e], v = V[e];
-  moments(c, ld_elem(G, e, gdt), m, v);
-  const float w = updated(c, step, decay, ld_elem(W, e, wdt), m, v);
-  M[e] = m;
-  V[e] = v;
-  st_elem(W, e, wdt, w);
-}
-
-template <int N>
-__global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ Adamw32Params<N> p) {
-  const int tile = blockIdx.x;
-  const int t = find_group(p.starts, p.h.count, tile);
-  const Coef c = coefficients(p.h);
-  if (c.skip) return;
-  const float lr = c.lr * p.lr_mult[t];
-  const float step = lr * c.inv_bc1, decay = fmaf(-lr, c.wd * p.decay_mult[t], 1.f);
-  const int flags = p.flags[t];
-  const int wdt = flags & MF_W_FP32 ? DT_FP32 : DT_BF16, gdt = flags & MF_G_FP32 ? DT_FP32 : DT_BF16;
-  const int64_t n = p.n[t];
-  void* W = p.W[t];
-  const void* G = p.G[t];
-  float* M = p.M[t];
-  float* V = p.V[t];
-  const int64_t base = (int64_t)(tile - p.starts[t]) * ADAMW32_TILE;
-  if (!(flags & MF_VEC)) {
-    for (int q = 0; q < 8; ++q) {
-      const int64_t e = base + q * THREADS + threadIdx.x;
-      if (e < n) adamw32_elem(W, G, M, V, wdt, gdt, e, c, step, decay);
-    }
-    return;
-  }
-  const int64_t e = base + threadIdx.x * 8 - ((flags >> MF_SHIFT_BIT) & 7);
-  if (e < 0 || e + 8 > n) {
-    for (int q = 0; q < 8; ++q)
-      if (e + q >= 0 && e + q < n) adamw32_elem(W, G, M, V, wdt, gdt, e + q, c, step, decay);
-    return;
-  }
-  float g[8], m[8], v[8], w[8];
-  ld8(G, e, gdt, g);
-  ld8(M, e, DT_FP32, m);
-  ld8(V, e, DT_FP32, v);
-  ld8(W, e, wdt, w);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    moments(c, g[q], m[q], v[q]);
-    w[q] = updated(c, step, decay, w[q], m[q], v[q]);
-  }
-  st8(M, e, DT_FP32, m);
-  st8(V, e, DT_FP32, v);
-  st8(W, e, wdt, w);
-}
-
-// ---------------------------------------------------------------------------
-// 8-bit moments.  A thread takes 16 consecutive elements at a time, so 8
-// threads of a warp share the scale of a block of 128.
-// ---------------------------------------------------------------------------
 // Two fp32 numbers in one 64-bit register pair, for the packed fp32
 // instructions: half the issue slots of the separate ones, the same rounding.
 struct F2 {
@@ -179,6 +96,113 @@ __device__ __forceinline__ float rcp_ftz(float x) {
   return r;
 }
 
+template <int DT>
+__device__ __forceinline__ void* elem_ptr(const void* p, int64_t e) {
+  return const_cast<char*>(reinterpret_cast<const char*>(p)) + e * (DT == DT_BF16 ? 2 : 4);
+}
+
+// ---------------------------------------------------------------------------
+// fp32 moments.  A thread takes 8 consecutive elements at a time; group k of a
+// tensor covers elements 8k - shift .. 8k - shift + 7, so that whole groups lie
+// on 32-byte boundaries in fp32 (16 in bf16) whatever the tensor's offset.
+// ---------------------------------------------------------------------------
+// The step for two elements.  The moments' products and sums are rounded one
+// by one, as in the 8-bit form (there they are part of its definition); square
+// root and reciprocal are the approximate ones (2^-23: they touch the update only).
+struct Step {
+  F2 gs, b1, c1, b2, c2, isb2, eps, nstep, decay;
+};
+__device__ __forceinline__ void update2(const Step& s, F2 g, F2& m, F2& v, F2& w) {
+  g = mul2(g, s.gs);
+  m = add2(mul2(m, s.b1), mul2(g, s.c1));
+  v = add2(mul2(v, s.b2), mul2(mul2(g, g), s.c2));
+  const float2 f = split(v), d = split(fma2(f2(sqrt_ftz(f.x), sqrt_ftz(f.y)), s.isb2, s.eps));
+  w = fma2(mul2(m, s.nstep), f2(rcp_ftz(d.x), rcp_ftz(d.y)), mul2(w, s.decay));
+}
+
+// 8 elements as pairs.
+template <int DT>
+__device__ __forceinline__ void ld4x2(const void* p, F2 x[4]) {
+  if (DT == DT_BF16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      x[q] = f2(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xffff0000u));
+  } else {
+    asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
+                 : "=l"(x[0].v), "=l"(x[1].v), "=l"(x[2].v), "=l"(x[3].v)
+                 : "l"(p));
+  }
+}
+template <int DT>
+__device__ __forceinline__ void st4x2(void* p, const F2 x[4]) {
+  if (DT == DT_BF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 f = split(x[q]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+      w[q] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(x[0].v), "l"(x[1].v),
+                 "l"(x[2].v), "l"(x[3].v)
+                 : "memory");
+  }
+}
+
+template <int N, int WDT, int GDT>
+__global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ Adamw32Params<N> p) {
+  const int tile = blockIdx.x;
+  const int t = find_group(p.starts, p.h.count, tile);
+  const Coef c = coefficients(p.h);
+  if (c.skip) return;
+  const int flags = p.flags[t];
+  // the CTA's elements, counted from its first group (which may begin before the tensor)
+  const int64_t first = (int64_t)(tile - p.starts[t]) * ADAMW32_TILE - ((flags >> MF_SHIFT_BIT) & 7);
+  const int left = (int)min(p.n[t] - first, (int64_t)ADAMW32_TILE);
+  const int lo = first < 0 ? (int)-first : 0;
+  const void* G = elem_ptr<GDT>(p.G[t], first);
+  void* W = elem_ptr<WDT>(p.W[t], first);
+  float* M = p.M[t] + first;
+  float* V = p.V[t] + first;
+  const float lr = c.lr * p.lr_mult[t];
+  const Step s = {f2(c.gs), f2(c.b1), f2(c.c1), f2(c.b2), f2(c.c2), f2(c.isb2), f2(c.eps),
+                  f2(-(lr * c.inv_bc1)), f2(fmaf(-lr, c.wd * p.decay_mult[t], 1.f))};
+  auto one = [&](uint32_t e) {
+    F2 m = f2(M[e]), v = f2(V[e]), w = f2(ld_elem(W, e, WDT));
+    update2(s, f2(ld_elem(G, e, GDT)), m, v, w);
+    M[e] = split(m).x;
+    V[e] = split(v).x;
+    st_elem(W, e, WDT, split(w).x);
+  };
+  if (!(flags & MF_VEC)) {
+    for (uint32_t e = threadIdx.x; e < (uint32_t)left; e += THREADS) one(e);
+    return;
+  }
+  const int e = threadIdx.x * 8;
+  if (e < lo || e + 8 > left) {  // a group that is not all inside
+    for (int i = max(e, lo); i < min(e + 8, left); ++i) one(i);
+    return;
+  }
+  F2 g[4], m[4], v[4], w[4];
+  ld4x2<GDT>(elem_ptr<GDT>(G, e), g);
+  ld4x2<DT_FP32>(M + e, m);
+  ld4x2<DT_FP32>(V + e, v);
+  ld4x2<WDT>(elem_ptr<WDT>(W, e), w);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) update2(s, g[q], m[q], v[q], w[q]);
+  st4x2<DT_FP32>(M + e, m);
+  st4x2<DT_FP32>(V + e, v);
+  st4x2<WDT>(elem_ptr<WDT>(W, e), w);
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit moments.  A thread takes 16 consecutive elements at a time, so 8
+// threads of a warp share the scale of a block of 128.
+// ---------------------------------------------------------------------------
 // Rounding to codes.  x in units of its code's format, multiplied by 2^-120
 // (e4m3) or 2^-112 (e5m2), lies where the fp32 exponent field counts like the
 // code's: the code's bits then stand in the fp32 pattern 20 (21) places up, the
@@ -203,22 +227,20 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {  // over 8 neighbour
   return v;
 }
 
-template <int DT>
-__device__ __forceinline__ void* elem_ptr(const void* p, int64_t e) {
-  return const_cast<char*>(reinterpret_cast<const char*>(p)) + e * (DT == DT_BF16 ? 2 : 4);
-}
-
 // 16 elements of a buffer as they lie in memory: `cnt` of them from element
-// e on, zero bits behind; `vec`: all 16, on a 16-byte boundary.
+// e on, zero bits behind; `vec`: all 16, on a 32-byte boundary.
 template <int DT>
 struct Raw16 {
   static constexpr int WORDS = DT == DT_BF16 ? 8 : 16;
   uint32_t w[WORDS];
   __device__ __forceinline__ void load(const void* p, uint32_t e, int cnt, bool vec) {
     if (vec) {
-      const uint4* q = reinterpret_cast<const uint4*>(elem_ptr<DT>(p, e));
 #pragma unroll
-      for (int i = 0; i < WORDS / 4; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = q[i];
+      for (int i = 0; i < WORDS; i += 8)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]),
+                       "=r"(w[i + 5]), "=r"(w[i + 6]), "=r"(w[i + 7])
+                     : "l"(reinterpret_cast<const char*>(elem_ptr<DT>(p, e)) + 4 * i));
     } else if (DT == DT_BF16) {
       const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + e;
 #pragma unroll
@@ -248,9 +270,13 @@ struct Raw16 {
   }
   __device__ __forceinline__ void store(void* p, uint32_t e, int cnt, bool vec) const {
     if (vec) {
-      uint4* q = reinterpret_cast<uint4*>(elem_ptr<DT>(p, e));
 #pragma unroll
-      for (int i = 0; i < WORDS / 4; ++i) q[i] = *reinterpret_cast<const uint4*>(w + 4 * i);
+      for (int i = 0; i < WORDS; i += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                         reinterpret_cast<char*>(elem_ptr<DT>(p, e)) + 4 * i),
+                     "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                     "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                     : "memory");
     } else if (DT == DT_BF16) {
       uint16_t* q = reinterpret_cast<uint16_t*>(p) + e;
 #pragma unroll
@@ -438,8 +464,15 @@ __global__ void adamw_scalars(const AdamwScalarsParams p) {
 }  // namespace
 
 template <int N>
-cudaError_t launch_adamw32(const Adamw32Params<N>& p, int tiles, cudaStream_t s) {
-  adamw32_step<N><<<tiles, THREADS, 0, s>>>(p);
+cudaError_t launch_adamw32(const Adamw32Params<N>& p, int wdt, int gdt, int grid, cudaStream_t s) {
+  if (wdt == DT_BF16 && gdt == DT_BF16)
+    adamw32_step<N, DT_BF16, DT_BF16><<<grid, THREADS, 0, s>>>(p);
+  else if (wdt == DT_BF16)
+    adamw32_step<N, DT_BF16, DT_FP32><<<grid, THREADS, 0, s>>>(p);
+  else if (gdt == DT_BF16)
+    adamw32_step<N, DT_FP32, DT_BF16><<<grid, THREADS, 0, s>>>(p);
+  else
+    adamw32_step<N, DT_FP32, DT_FP32><<<grid, THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <int N>
@@ -458,8 +491,8 @@ cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s) {
   adamw_scalars<<<1, 1, 0, s>>>(p);
   return cudaGetLastError();
 }
-template cudaError_t launch_adamw32(const Adamw32Params<MANY_SMALL>&, int, cudaStream_t);
-template cudaError_t launch_adamw32(const Adamw32Params<MANY_MAX>&, int, cudaStream_t);
+template cudaError_t launch_adamw32(const Adamw32Params<MANY_SMALL>&, int, int, int, cudaStream_t);
+template cudaError_t launch_adamw32(const Adamw32Params<MANY_MAX>&, int, int, int, cudaStream_t);
 template cudaError_t launch_adamw8(const Adamw8Params<MANY_SMALL>&, int, int, int, cudaStream_t);
 template cudaError_t launch_adamw8(const Adamw8Params<MANY_MAX>&, int, int, int, cudaStream_t);
 
