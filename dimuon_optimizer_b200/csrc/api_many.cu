@@ -29,10 +29,12 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 size_t elem_size(int32_t dt) { return dt == DM_FP32 ? 4 : 2; }
 bool bad_dtype(int32_t dt) { return dt != DM_BF16 && dt != DM_FP32; }
 
-// Element offset (0..7) of a buffer from the last address whose element number is a multiple of 8.
-int offset8(const void* p, size_t esz) { return (int)(reinterpret_cast<uintptr_t>(p) / esz % 8); }
+// Element offset of a buffer from the last address whose element number is a multiple of `m`.
+int offset_in(const void* p, size_t esz, int m) {
+  return (int)(reinterpret_cast<uintptr_t>(p) / esz % m);
+}
 
-// Whether an output address occurs twice: an open-addressing table of all of them.
+// Buffer addresses of a call (an open-addressing table), to find those that occur twice.
 class AddressSet {
  public:
   explicit AddressSet(size_t count) {
@@ -41,15 +43,20 @@ class AddressSet {
     slots_.assign(cap, nullptr);
   }
   bool insert(const void* p) {  // false: it is there already
-    const size_t mask = slots_.size() - 1;
-    size_t i = (size_t)((reinterpret_cast<uintptr_t>(p) >> 1) * 0x9E3779B97F4A7C15ull >> 20) & mask;
-    for (; slots_[i]; i = (i + 1) & mask)
-      if (slots_[i] == p) return false;
+    const size_t i = find(p);
+    if (slots_[i]) return false;
     slots_[i] = p;
     return true;
   }
+  bool has(const void* p) const { return slots_[find(p)] != nullptr; }
 
  private:
+  size_t find(const void* p) const {  // its slot, or the free one it would take
+    const size_t mask = slots_.size() - 1;
+    size_t i = (size_t)((reinterpret_cast<uintptr_t>(p) >> 1) * 0x9E3779B97F4A7C15ull >> 20) & mask;
+    while (slots_[i] && slots_[i] != p) i = (i + 1) & mask;
+    return i;
+  }
   std::vector<const void*> slots_;
 };
 
@@ -95,6 +102,7 @@ dm_status_t validate(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparams_
   return DM_OK;
 }
 
+// No buffer is written twice, none that is written is a gradient.
 bool outputs_distinct(const dm_adamw_tensor_t* ts, int n) {
   AddressSet seen((size_t)n * 5);
   for (int i = 0; i < n; ++i) {
@@ -103,18 +111,20 @@ bool outputs_distinct(const dm_adamw_tensor_t* ts, int n) {
     if (!seen.insert(t.weight) || !seen.insert(t.moment1) || !seen.insert(t.moment2)) return false;
     if (t.state == DM_STATE_8BIT && (!seen.insert(t.scale1) || !seen.insert(t.scale2))) return false;
   }
+  for (int i = 0; i < n; ++i)
+    if (ts[i].numel > 0 && seen.has(ts[i].grad)) return false;
   return true;
 }
 
 uint8_t adamw_flags(const dm_adamw_tensor_t& t) {
   const size_t wsz = elem_size(t.weight_dtype), gsz = elem_size(t.grad_dtype);
   int f = (t.weight_dtype == DM_FP32 ? MF_W_FP32 : 0) | (t.grad_dtype == DM_FP32 ? MF_G_FP32 : 0);
-  const int s = offset8(t.weight, wsz);
+  const int s = offset_in(t.weight, wsz, 8);
   if (t.state == DM_STATE_8BIT) {
     if (aligned(t.weight, 32) && aligned(t.grad, 32) && aligned(t.moment1, 16) &&
         aligned(t.moment2, 16))
       f |= MF_VEC;
-  } else if (offset8(t.grad, gsz) == s && offset8(t.moment1, 4) == s && offset8(t.moment2, 4) == s) {
+  } else if (offset_in(t.grad, gsz, 8) == s && offset_in(t.moment1, 4, 8) == s && offset_in(t.moment2, 4, 8) == s) {
     f |= MF_VEC | s << MF_SHIFT_BIT;
   }
   return (uint8_t)f;
@@ -122,14 +132,16 @@ uint8_t adamw_flags(const dm_adamw_tensor_t& t) {
 
 // Tiles of a tensor in its launch (vector groups start `shift` elements early).
 int64_t tile_count(int64_t numel, int flags, int tile) {
-  return ceil_div(numel + ((flags >> MF_SHIFT_BIT) & 7), tile);
+  return ceil_div(numel + ((flags >> MF_SHIFT_BIT) & 15), tile);
 }
 
 // Launches over the tensors of `order` (indices with work), in that order:
 // fill(params, slot, index) for each, then go(params, tiles) per launch.
-template <class Small, class Large, class Tiles, class Fill, class Go>
-dm_status_t in_launches(const std::vector<int>& order, Small& small, Large& large, Tiles tiles_of,
-                        Fill fill, Go go) {
+template <template <int> class Params, class Tiles, class Fill, class Go>
+dm_status_t in_launches(const std::vector<int>& order, Tiles tiles_of, Fill fill, Go go) {
+  static thread_local Params<MANY_SMALL> small;
+  static thread_local Params<MANY_MID> mid;
+  static thread_local Params<MANY_MAX> large;
   for (size_t b = 0; b < order.size();) {
     size_t e = b;
     int64_t tiles = 0;
@@ -149,7 +161,8 @@ dm_status_t in_launches(const std::vector<int>& order, Small& small, Large& larg
       p.starts[e - b] = (int)at;
       return go(p, (int)(e - b), (int)at);
     };
-    const cudaError_t err = (int)(e - b) <= MANY_SMALL ? run(small) : run(large);
+    const int count = (int)(e - b);
+    const cudaError_t err = count <= MANY_SMALL ? run(small) : count <= MANY_MID ? run(mid) : run(large);
     if (err != cudaSuccess) return DM_ERR_CUDA;
     b = e;
   }
@@ -220,10 +233,8 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
         p.decay_mult[q] = t.decay_mult;
       };
       if (!fp32.empty()) {
-        static thread_local Adamw32Params<MANY_SMALL> small;
-        static thread_local Adamw32Params<MANY_MAX> large;
-        st = in_launches(
-            fp32, small, large,
+        st = in_launches<Adamw32Params>(
+            fp32,
             [&](int i) { return tile_count(ts[i].numel, adamw_flags(ts[i]), ADAMW32_TILE); },
             [&](auto& p, int q, int i) {
               common(p, q, i);
@@ -240,11 +251,9 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
         if (st != DM_OK) return st;
       }
       if (!eight.empty()) {
-        static thread_local Adamw8Params<MANY_SMALL> small;
-        static thread_local Adamw8Params<MANY_MAX> large;
         const int tile = elems8 >= ADAMW8_LONG ? 4 * ADAMW8_PASS : ADAMW8_PASS;
-        st = in_launches(
-            eight, small, large, [&](int i) { return tile_count(ts[i].numel, 0, tile); },
+        st = in_launches<Adamw8Params>(
+            eight, [&](int i) { return tile_count(ts[i].numel, 0, tile); },
             [&](auto& p, int q, int i) {
               common(p, q, i);
               p.M[q] = ts[i].moment1;
@@ -283,11 +292,11 @@ dm_status_t validate(const dm_grad_t* ts, int n) {
 }
 
 uint8_t clip_flags(const dm_grad_t& t, bool with_out) {
-  const int s = offset8(t.grad, elem_size(t.grad_dtype));
+  const int s = offset_in(t.grad, elem_size(t.grad_dtype), 16);
   int f = (t.grad_dtype == DM_FP32 ? MF_G_FP32 : 0) | s << MF_SHIFT_BIT | MF_VEC;
   if (with_out) {
     if (t.out_dtype == DM_FP32) f |= MF_W_FP32;
-    if (offset8(t.out, elem_size(t.out_dtype)) != s) f &= ~(MF_VEC | 7 << MF_SHIFT_BIT);
+    if (offset_in(t.out, elem_size(t.out_dtype), 16) != s) f &= ~(MF_VEC | 15 << MF_SHIFT_BIT);
   }
   return (uint8_t)f;
 }
@@ -298,7 +307,7 @@ int64_t clip_launches(const dm_grad_t* ts, int n) {
   int64_t launches = 0, count = 0, tiles = 0;
   for (int i = 0; i < n; ++i) {
     if (ts[i].numel == 0) continue;
-    const int64_t k = tile_count(ts[i].numel, 7 << MF_SHIFT_BIT, CLIP_TILE);
+    const int64_t k = tile_count(ts[i].numel, 15 << MF_SHIFT_BIT, CLIP_TILE);
     if (count == 0 || count == MANY_MAX || tiles + k > MAX_TILES) {
       ++launches;
       count = tiles = 0;
@@ -320,29 +329,33 @@ dm_status_t grad_clip(const dm_grad_t* ts, int n, float max_norm, float* result,
   if (!(max_norm > 0.f) || !result || !aligned(result, 4)) return DM_ERR_INVALID_ARG;
   st = check_workspace(ws_v, ws_bytes, clip_bytes(ts, n));
   if (st != DM_OK) return st;
-  std::vector<int> all, with_out;
-  AddressSet seen((size_t)n);
+  std::vector<int> all, with_out[4];  // by the two types
+  // an output is written once, and is no gradient but its own, and then of no other tensor
+  AddressSet outs((size_t)n), grads((size_t)n), repeated((size_t)n);
+  for (int i = 0; i < n; ++i)
+    if (ts[i].numel > 0 && !grads.insert(ts[i].grad)) repeated.insert(ts[i].grad);
   for (int i = 0; i < n; ++i) {
     if (ts[i].numel == 0) continue;
     all.push_back(i);
-    if (!ts[i].out) continue;
-    if (!seen.insert(ts[i].out)) return DM_ERR_INVALID_ARG;
-    with_out.push_back(i);
+    const void* out = ts[i].out;
+    if (!out) continue;
+    if (!outs.insert(out) || (grads.has(out) && (out != ts[i].grad || repeated.has(out))))
+      return DM_ERR_INVALID_ARG;
+    with_out[ts[i].grad_dtype * 2 + ts[i].out_dtype].push_back(i);
   }
   uint8_t* ws = reinterpret_cast<uint8_t*>(ws_v);
   double* part = reinterpret_cast<double*>(ws + HEADER_BYTES);
-  static thread_local ClipParams<MANY_SMALL> small;
-  static thread_local ClipParams<MANY_MAX> large;
   int n_part = 0;
   auto pass = [&](const std::vector<int>& order, bool out) {
-    return in_launches(
-        order, small, large,
-        [&](int i) { return tile_count(ts[i].numel, clip_flags(ts[i], out), CLIP_TILE); },
+    auto flags = [&](int i) { return clip_flags(ts[i], out); };
+    return in_launches<ClipParams>(
+        order,
+        [&](int i) { return tile_count(ts[i].numel, flags(i), CLIP_TILE); },
         [&](auto& p, int q, int i) {
           p.G[q] = ts[i].grad;
           p.out[q] = ts[i].out;
           p.n[q] = ts[i].numel;
-          p.flags[q] = clip_flags(ts[i], out);
+          p.flags[q] = flags(i);
         },
         [&](auto& p, int count, int tiles) {
           p.count = count;
@@ -354,7 +367,7 @@ dm_status_t grad_clip(const dm_grad_t* ts, int n, float max_norm, float* result,
           if (out) {
             p.part = part;
             p.n_part = n_part;
-            return launch_grad_write(p, grid, s);
+            return launch_grad_write(p, ts[order[0]].grad_dtype, ts[order[0]].out_dtype, grid, s);
           }
           p.part = part + n_part;
           n_part += grid;
@@ -363,14 +376,15 @@ dm_status_t grad_clip(const dm_grad_t* ts, int n, float max_norm, float* result,
   };
   st = pass(all, false);
   if (st != DM_OK) return st;
-  if (!with_out.empty()) return pass(with_out, true);
-  small.count = small.tiles = 0;
-  small.max_norm = max_norm;
-  small.result = result;
-  small.status = reinterpret_cast<int*>(ws);
-  small.part = part;
-  small.n_part = n_part;
-  DM_CUDA(launch_grad_finish(small, s));
+  bool written = false;
+  for (const std::vector<int>& list : with_out) {
+    if (list.empty()) continue;
+    st = pass(list, true);
+    if (st != DM_OK) return st;
+    written = true;
+  }
+  if (written) return DM_OK;
+  DM_CUDA(launch_grad_finish(part, n_part, max_norm, result, reinterpret_cast<int*>(ws), s));
   return DM_OK;
 }
 

@@ -8,18 +8,20 @@
 
 namespace dm {
 
-// Tensors per launch.  The parameters are copied at every launch, so short
+// Tensors per launch.  The parameters are copied at every launch, so shorter
 // lists take a smaller block.
 constexpr int MANY_SMALL = 24;
+constexpr int MANY_MID = 160;
 constexpr int MANY_MAX = 448;
 
-// Per-tensor flags: types, and the element offset (0..7) of the tensor from a
-// 32-byte boundary of fp32 that all its buffers share.
+// Per-tensor flags: types, and the element offset of the tensor that all its
+// buffers share (AdamW: 0..7, from a multiple of 8 elements; clipping: 0..15, from
+// a multiple of 16).
 enum {
   MF_W_FP32 = 1,     // weight (or out) is fp32, else bf16
   MF_G_FP32 = 2,     // grad is fp32, else bf16
   MF_VEC = 4,        // all buffers share one offset: vector path
-  MF_SHIFT_BIT = 4   // bits 4-6: that offset
+  MF_SHIFT_BIT = 4   // bits 4-7: that offset
 };
 
 // ------------------------------- AdamW ------------------------------------
@@ -104,8 +106,9 @@ __host__ __device__ inline uint32_t many_mix(uint32_t x) {
 constexpr uint32_t MANY_GOLDEN = 0x9E3779B9u;  // 2^32 / golden ratio, odd
 
 // ----------------------------- grad clip ----------------------------------
-constexpr int CLIP_TILE = 4096;       // elements per CTA pass, 16 per thread
-constexpr int CLIP_MAX_GRID = 1184;   // CTAs (partial sums) per launch of the norm pass
+constexpr int CLIP_GROUPS = 4;                     // 16-element groups of a thread in a tile
+constexpr int CLIP_TILE = 256 * 16 * CLIP_GROUPS;  // elements of a tile: one CTA of 256 threads
+constexpr int CLIP_MAX_GRID = 1184;                // CTAs of a launch (partial sums of the norm pass)
 
 template <int N>
 struct ClipParams {
@@ -127,7 +130,8 @@ static_assert(sizeof(ClipParams<MANY_MAX>) <= 32764, "kernel parameter space");
 template <int N>
 cudaError_t launch_grad_sumsq(const ClipParams<N>& p, int grid, cudaStream_t s);
 template <int N>
-cudaError_t launch_grad_write(const ClipParams<N>& p, int grid, cudaStream_t s);
-cudaError_t launch_grad_finish(const ClipParams<MANY_SMALL>& p, cudaStream_t s);
+cudaError_t launch_grad_write(const ClipParams<N>& p, int gdt, int odt, int grid, cudaStream_t s);
+cudaError_t launch_grad_finish(const double* part, int n_part, float max_norm, float* result,
+                               int* status, cudaStream_t s);
 
 }  // namespace dm

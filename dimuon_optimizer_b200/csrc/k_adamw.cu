@@ -492,8 +492,10 @@ cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 template cudaError_t launch_adamw32(const Adamw32Params<MANY_SMALL>&, int, int, int, cudaStream_t);
+template cudaError_t launch_adamw32(const Adamw32Params<MANY_MID>&, int, int, int, cudaStream_t);
 template cudaError_t launch_adamw32(const Adamw32Params<MANY_MAX>&, int, int, int, cudaStream_t);
 template cudaError_t launch_adamw8(const Adamw8Params<MANY_SMALL>&, int, int, int, cudaStream_t);
+template cudaError_t launch_adamw8(const Adamw8Params<MANY_MID>&, int, int, int, cudaStream_t);
 template cudaError_t launch_adamw8(const Adamw8Params<MANY_MAX>&, int, int, int, cudaStream_t);
 
 }  // namespace dm

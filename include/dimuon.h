@@ -306,9 +306,10 @@ dm_status_t dm_step_noalloc(const dm_matrix_t* mats, int n,
  *     type only; buffers whose addresses are at the same element offset from
  *     a 32-byte boundary (all of them aligned, or views at one offset of flat
  *     buffers) take the vector path.
- *   - No element may be written twice in one call: a buffer that appears as an
- *     output of two tensors is rejected (equal addresses are detected; the
- *     caller answers for partial overlaps).
+ *   - No element may be written twice in one call, nor read as a gradient and
+ *     written (but by a tensor of dm_grad_clip whose out is its own grad): such
+ *     buffers are rejected with DM_ERR_INVALID_ARG when their addresses are
+ *     equal; the caller answers for partial overlaps.
  * ======================================================================== */
 
 /* How a tensor's two moments are held.

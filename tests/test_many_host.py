@@ -99,12 +99,21 @@ def test_the_same_tensor_twice_is_refused():
     assert dm.dm_adamw_step([a, b], hp, WS, stream=0) == dm.DM_ERR_INVALID_ARG
     assert dm.dm_adamw_step([a, a], hp, WS, stream=0) == dm.DM_ERR_INVALID_ARG
     g = fake_grad(out=0x70000)
-    res = c_floats()
-    assert clip([g, g], 1.0, res) == dm.DM_ERR_INVALID_ARG
+    assert clip([g, g], 1.0, 0x200000) == dm.DM_ERR_INVALID_ARG
 
 
-def c_floats():
-    return 0x200000  # never dereferenced: the calls below are refused
+def test_gradients_that_are_written_are_refused():
+    hp = dm.dm_adamw_default_hparams()
+    a, b = fake_tensor(), fake_tensor(at=0x100000)
+    b.grad = a.weight
+    assert dm.dm_adamw_step([a, b], hp, WS, stream=0) == dm.DM_ERR_INVALID_ARG
+    # one tensor's output is another's gradient; a gradient in place that another reads
+    x, y = fake_grad(out=0x20000), fake_grad()
+    y.grad = 0x20000
+    assert clip([x, y], 1.0, 0x200000) == dm.DM_ERR_INVALID_ARG
+    assert clip([y, x], 1.0, 0x200000) == dm.DM_ERR_INVALID_ARG
+    x, y = fake_grad(out=0x10000), fake_grad(out=0x20000)
+    assert clip([x, y], 1.0, 0x200000) == dm.DM_ERR_INVALID_ARG
 
 
 def clip(ts, max_norm, result, ws=WS):
