@@ -69,10 +69,12 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+// A sum of two products that stay rounded: as two separate additions, because
+// the assembler joins a packed product and a packed sum into one packed
+// multiply-add, their .rn and --fmad=false notwithstanding (it costs 1.5 %).
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
+  const float2 x = split(a), y = split(b);
+  return f2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;

@@ -383,7 +383,9 @@ void dm_adamw_default_hparams(dm_adamw_hparams_t* hp);
 dm_status_t dm_adamw_workspace_size(const dm_adamw_tensor_t* tensors, int n,
                                     const dm_adamw_hparams_t* hp, size_t* bytes);
 
-/* One AdamW step over the tensors, per element, in fp32:
+/* One AdamW step over the tensors, per element, in fp32 (g, m' and v' with
+ * every product and sum rounded by itself, so that they are the same bits in
+ * any implementation, and the 8-bit codes with them):
  *   g  = grad * grad_scale
  *   m' = beta1 m + (1 - beta1) g
  *   v' = beta2 v + (1 - beta2) g^2

@@ -198,6 +198,41 @@ def test_8bit_blocks_of_extreme_range():
         h = (ao.unpack(c1, s1, ao.E4M3), ao.unpack(c2, s2, ao.E5M2))
 
 
+@pytest.mark.parametrize("wdt,gdt", [(BF, BF), (F32, F32)])
+def test_moments_are_rounded_product_by_product(wdt, gdt):
+    """The new moments' bits are those of separate fp32 products and sums (a
+    multiply-add in their place changes a quarter of them), and so are the
+    8-bit codes, also where a block's largest moment lies at a scale's border."""
+    n = 1 << 18
+    rng = np.random.default_rng(31)
+    gs = torch.tensor([0.37], device="cuda")
+    hp = dm.dm_adamw_default_hparams(grad_scale=gs, step=5, seed=8)
+    p = ao.AdamWParams(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay)
+    W, G = (torch.from_numpy(rng.standard_normal(n)).float().cuda() for _ in "wg")
+    W, G = W.to(wdt), G.to(gdt)
+    m, v = (torch.from_numpy(x).float().cuda() for x in (rng.standard_normal(n), rng.random(n)))
+    h = [to_host(x) for x in (G, m, v)]
+    ts = [dm.dm_adamw_tensor(W, G, m, v)]
+    dm.check(dm.dm_adamw_step(ts, hp, workspace(ts, hp)))
+    m32, v32 = ao.moments_f32(*h, p, 0.37)
+    assert np.array_equal(to_host(m), m32) and np.array_equal(to_host(v), v32)
+    st = dm.dm_adamw_state(W, dm.DM_STATE_8BIT)
+    st[0].view(torch.uint8).copy_(torch.from_numpy(rng.integers(0, 127, n, dtype=np.uint8)))
+    st[1].view(torch.uint8).copy_(torch.from_numpy(rng.integers(0, 124, n, dtype=np.uint8)))
+    st[2].fill_(2.0 ** -9)
+    st[3].fill_(2.0 ** -17)
+    before = (ao.unpack(st[0].view(torch.uint8).cpu().numpy(), to_host(st[2]), ao.E4M3),
+              ao.unpack(st[1].view(torch.uint8).cpu().numpy(), to_host(st[3]), ao.E5M2))
+    ts = [dm.dm_adamw_tensor(W, G, *st)]
+    dm.check(dm.dm_adamw_step(ts, hp, workspace(ts, hp)))
+    m32, v32 = ao.moments_f32(h[0], *before, p, 0.37)
+    c1, s1, c2, s2 = ao.pack_moments(m32.astype(float), v32.astype(float), 8, 5, 0)
+    np.testing.assert_array_equal(to_host(st[2]), s1)
+    np.testing.assert_array_equal(to_host(st[3]), s2)
+    np.testing.assert_array_equal(st[0].view(torch.uint8).cpu().numpy(), c1)
+    np.testing.assert_array_equal(st[1].view(torch.uint8).cpu().numpy(), c2)
+
+
 def test_many_tensors_and_both_states_in_one_call():
     """More tensors than one launch holds, the two state formats mixed; the
     8-bit noise goes by the position in the call."""
