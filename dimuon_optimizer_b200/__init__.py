@@ -407,6 +407,8 @@ def dm_adamw_workspace_size(tensors, hp):
 def dm_adamw_step(tensors, hp, workspace, stream=None):
     """One AdamW step over the tensors (include/dimuon.h).  The caller counts
     the steps in hp.step, or gives hp a device step_counter."""
+    if hasattr(workspace, "data_ptr"):
+        _on_device(workspace)
     arr, n = _list(tensors, dm_adamw_tensor_t)
     ptr, nbytes = _ws(workspace)
     return _lib.dm_adamw_step(arr, n, ctypes.byref(hp), ptr, nbytes, _stream_handle(stream))
@@ -445,7 +447,7 @@ def dm_grad_clip(tensors, max_norm, result, workspace, stream=None):
     import torch
     if result.numel() != 2 or result.dtype != torch.float32:
         raise ValueError("result must be an fp32 tensor of two elements")
-    _on_device(result)
+    _on_device(result, workspace if hasattr(workspace, "data_ptr") else None)
     arr, n = _list(tensors, dm_grad_t)
     ptr, nbytes = _ws(workspace)
     return _lib.dm_grad_clip(arr, n, float(max_norm), c_void_p(result.data_ptr()), ptr, nbytes,

@@ -188,6 +188,8 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
   h.b2 = hp->beta2;
   h.c2 = (float)(1.0 - (double)hp->beta2);
   h.eps = hp->eps;
+  // sqrt(2^-126) times the largest 1 / sqrt(1 - beta2^t) below half a place of eps
+  h.flush = 0x1p-63 / std::sqrt(1.0 - (double)hp->beta2) <= 0x1p-24 * (double)hp->eps;
   h.lr_dev = hp->lr_dev;
   h.grad_scale = hp->grad_scale;
   h.status = status;

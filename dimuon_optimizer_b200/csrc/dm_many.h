@@ -41,6 +41,8 @@ struct AdamwScalars {
 struct AdamwHead {
   int count;
   int write_status;          // host-counted step: block 0 writes the status word
+  int flush;                 // eps is so large that the root of a subnormal second moment vanishes
+                             // beside it
   float lr, wd, b1, c1, b2, c2, eps;
   AdamwScalars sc;
   const AdamwScalars* dev;   // null: sc above

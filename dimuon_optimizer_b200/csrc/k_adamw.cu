@@ -87,9 +87,15 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float sqrt_ftz(float x) {
+// FLUSH takes subnormal numbers for zero: one instruction instead of four, for an eps next to
+// which their square roots vanish.
+template <bool FLUSH>
+__device__ __forceinline__ float sqrt_approx(float x) {
   float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  if (FLUSH)
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float rcp_ftz(float x) {
@@ -118,7 +124,7 @@ __device__ __forceinline__ void update2(const Step& s, F2 g, F2& m, F2& v, F2& w
   g = mul2(g, s.gs);
   m = add2(mul2(m, s.b1), mul2(g, s.c1));
   v = add2(mul2(v, s.b2), mul2(mul2(g, g), s.c2));
-  const float2 f = split(v), d = split(fma2(f2(sqrt_ftz(f.x), sqrt_ftz(f.y)), s.isb2, s.eps));
+  const float2 f = split(v), d = split(fma2(f2(sqrt_approx<false>(f.x), sqrt_approx<false>(f.y)), s.isb2, s.eps));
   w = fma2(mul2(m, s.nstep), f2(rcp_ftz(d.x), rcp_ftz(d.y)), mul2(w, s.decay));
 }
 
@@ -155,6 +161,11 @@ __device__ __forceinline__ void st4x2(void* p, const F2 x[4]) {
   }
 }
 
+// Bound by HBM: 262 M elements (bf16 weights and gradients, 22 bytes each) take
+// 834 us, 6.93 TB/s or 1.06 of the measured copy; 448 tensors of 32768 fp32
+// elements 63 us (1.00).  What made the difference were accesses of 32 bytes
+// per thread (16 bytes at a stride of 32 before: 924 and 70 us) and types fixed
+// per launch; one pass per CTA (2, 4, 8 passes: 849, 859, 875 us).
 template <int N, int WDT, int GDT>
 __global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ Adamw32Params<N> p) {
   const int tile = blockIdx.x;
@@ -330,8 +341,8 @@ struct Codes16 {
 };
 
 // Bound by HBM up to the power limit: 262 M elements (bf16 weights and
-// gradients) take 400 us (6.66 TB/s) while the clock stays at 1.96 GHz, 449 us
-// (0.90 of the measured copy) in a long run, when the part reaches its 1000 W
+// gradients) take 396 us (6.72 TB/s) while the clock stays at 1.96 GHz, 447 us
+// (0.91 of the measured copy) in a long run, when the part reaches its 1000 W
 // and the clock falls to 1.6 GHz: 40 instructions per element then fill three
 // quarters of the issue slots.  The first form (one fp32 operation at a time,
 // separate code for the subnormal codes, one pass per CTA) took 88 instructions
@@ -342,8 +353,11 @@ struct Codes16 {
 // instead of 142 us on 448 tensors of 131072 elements).  Reading the next pass
 // into registers during this one made it twice as slow (128 registers).
 // Registers are held to 64, four CTAs per SM (without the limit 66 to 104 by
-// type: 458 us, and 182 instead of 173 us with 66 M fp32 weights and gradients).
-template <int N, int WDT, int GDT>
+// type: 458 instead of 449 us, and 182 instead of 173 us with 66 M fp32 weights
+// and gradients).  Accesses of 32 bytes instead of 16 gave the last 7 % (449 to 418 us).
+// FLUSH: see sqrt_approx (447 against 465 us in the long run; with fp32 moments the
+// instructions are hidden behind HBM, so that form has no such variant).
+template <int N, int WDT, int GDT, bool FLUSH>
 __global__ void __launch_bounds__(THREADS, 4)
     adamw8_step(const __grid_constant__ Adamw8Params<N> p) {
   const int tile = blockIdx.x;
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, 4)
       const float2 mf = split(m[q]), vf = split(v[q]);
       top1 = max3_abs(top1, mf.x, mf.y);
       top2 = max3_abs(top2, vf.x, vf.y);
-      const float2 d = split(fma2(f2(sqrt_ftz(vf.x), sqrt_ftz(vf.y)), isb2, eps));
+      const float2 d = split(fma2(f2(sqrt_approx<FLUSH>(vf.x), sqrt_approx<FLUSH>(vf.y)), isb2, eps));
       w.set(q, fma2(mul2(m[q], nstep), f2(rcp_ftz(d.x), rcp_ftz(d.y)), mul2(w.pair(q), decay)));
     }
     w.store(W, e, cnt, vec);
@@ -477,16 +491,23 @@ cudaError_t launch_adamw32(const Adamw32Params<N>& p, int wdt, int gdt, int grid
     adamw32_step<N, DT_FP32, DT_FP32><<<grid, THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
+template <int N, int WDT, int GDT>
+void run_adamw8(const Adamw8Params<N>& p, int grid, cudaStream_t s) {
+  if (p.h.flush)
+    adamw8_step<N, WDT, GDT, true><<<grid, THREADS, 0, s>>>(p);
+  else
+    adamw8_step<N, WDT, GDT, false><<<grid, THREADS, 0, s>>>(p);
+}
 template <int N>
 cudaError_t launch_adamw8(const Adamw8Params<N>& p, int wdt, int gdt, int grid, cudaStream_t s) {
   if (wdt == DT_BF16 && gdt == DT_BF16)
-    adamw8_step<N, DT_BF16, DT_BF16><<<grid, THREADS, 0, s>>>(p);
+    run_adamw8<N, DT_BF16, DT_BF16>(p, grid, s);
   else if (wdt == DT_BF16)
-    adamw8_step<N, DT_BF16, DT_FP32><<<grid, THREADS, 0, s>>>(p);
+    run_adamw8<N, DT_BF16, DT_FP32>(p, grid, s);
   else if (gdt == DT_BF16)
-    adamw8_step<N, DT_FP32, DT_BF16><<<grid, THREADS, 0, s>>>(p);
+    run_adamw8<N, DT_FP32, DT_BF16>(p, grid, s);
   else
-    adamw8_step<N, DT_FP32, DT_FP32><<<grid, THREADS, 0, s>>>(p);
+    run_adamw8<N, DT_FP32, DT_FP32>(p, grid, s);
   return cudaGetLastError();
 }
 cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s) {

@@ -83,7 +83,9 @@ typedef enum {
   DM_ERR_NONFINITE = 6,       /* device status: non-finite ||X_0||_F; that
                                  matrix got O = 0 (its W was only decayed).
                                  A norm below 1e-15 also gives O = 0, without
-                                 a status (nothing to normalise).             */
+                                 a status (nothing to normalise).
+                                 dm_adamw_step, dm_grad_clip: a non-finite
+                                 scalar or norm; nothing was updated.         */
   DM_ERR_CANARY = 7           /* device status (DM_DBG_CANARY only): a canary
                                  word between workspace regions was changed
                                  during the step                              */

@@ -344,6 +344,25 @@ def test_extreme_gradients():
 
 
 @pytest.mark.parametrize("state", [dm.DM_STATE_FP32, dm.DM_STATE_8BIT])
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+def test_tiny_eps_divides_by_subnormal_moments(state, eps):
+    """Gradients whose second moments are subnormal (1e-40): with eps next to
+    nothing the first step is still lr times the sign.  v = 1e-3 g^2 in steps of
+    2^-149 is off by half a step, 2^-150 / 1e-40 relative: the update by half of that."""
+    n = 1000
+    g = torch.full((n,), 10.0 ** -18.5, device="cuda")
+    g[::2] *= -1
+    W = torch.zeros(n, device="cuda")
+    st = dm.dm_adamw_state(W, state)
+    hp = dm.dm_adamw_default_hparams(lr=0.5, weight_decay=0.0, eps=eps)
+    ts = [dm.dm_adamw_tensor(W, g, *st)]
+    dm.check(dm.dm_adamw_step(ts, hp, workspace(ts, hp)))
+    want = -0.5 * np.sign(to_host(g))
+    # g^2 = 1e-37 is normal; its product with 1e-3 rounds to a multiple of 2^-149
+    assert np.all(np.abs(to_host(W) - want) <= 0.5 * (16 * U + 0.5 * 2.0 ** -150 / 1e-40))
+
+
+@pytest.mark.parametrize("state", [dm.DM_STATE_FP32, dm.DM_STATE_8BIT])
 def test_counted_steps_in_a_graph_equal_eager_steps(state):
     """A captured step with a device counter and learning rate, replayed, does
     what host-counted steps do, bit for bit."""
