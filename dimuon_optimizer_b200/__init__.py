@@ -204,6 +204,17 @@ def _list(items, struct):
     return (struct * max(1, len(items)))(*items), len(items)
 
 
+def _kept_array(items, struct):
+    """An array of the descriptors that keeps their tensors alive (an array
+    copies the addresses only)."""
+    items = list(items)
+    if not items:
+        return []
+    arr, _ = _list(items, struct)
+    arr._keep = [getattr(t, "_keep", None) for t in items]
+    return arr
+
+
 def _stream_handle(stream):
     if stream is None:
         import torch
@@ -338,7 +349,8 @@ def dm_adamw_state(weight, state=DM_STATE_FP32):
 
 def dm_adamw_tensor(weight, grad, moment1, moment2, scale1=None, scale2=None, lr_mult=1.0,
                     decay_mult=1.0):
-    """A dm_adamw_tensor_t over contiguous torch CUDA tensors of one size.
+    """A dm_adamw_tensor_t over contiguous torch CUDA tensors of one size,
+    which it keeps alive (moments made in the call included).
     The moments are fp32, or float8_e4m3fn and float8_e5m2 with one fp32
     scale per DM_ADAMW_BLOCK elements (scale1, scale2)."""
     import torch
@@ -366,13 +378,14 @@ def dm_adamw_tensor(weight, grad, moment1, moment2, scale1=None, scale2=None, lr
     t.weight, t.grad = weight.data_ptr(), grad.data_ptr()
     t.moment1, t.moment2 = moment1.data_ptr(), moment2.data_ptr()
     t.lr_mult, t.decay_mult = lr_mult, decay_mult
+    t._keep = (weight, grad, moment1, moment2, scale1, scale2)
     return t
 
 
 def dm_adamw_tensors(tensors):
     """The descriptors as one C array, for callers that keep it from step to
     step (a plain list is converted at every call)."""
-    return _list(tensors, dm_adamw_tensor_t)[0] if len(tensors) else []
+    return _kept_array(tensors, dm_adamw_tensor_t)
 
 
 def dm_adamw_default_hparams(**overrides):
@@ -415,8 +428,9 @@ def dm_adamw_step(tensors, hp, workspace, stream=None):
 
 
 def dm_grad_tensor(grad, out=None):
-    """A dm_grad_t over contiguous torch CUDA tensors; `out` (optional, of
-    either dtype, or `grad` itself) gets the clipped gradient."""
+    """A dm_grad_t over contiguous torch CUDA tensors, which it keeps alive;
+    `out` (optional, of either dtype, or `grad` itself) gets the clipped
+    gradient."""
     if out is not None and out.numel() != grad.numel():
         raise ValueError("grad and out must have the same number of elements")
     t = dm_grad_t()
@@ -424,12 +438,13 @@ def dm_grad_tensor(grad, out=None):
     if out is not None:
         t.out, t.out_dtype = out.data_ptr(), _dtype_code(out)
     _on_device(grad, out)
+    t._keep = (grad, out)
     return t
 
 
 def dm_grad_tensors(tensors):
     """The descriptors as one C array, for callers that keep it."""
-    return _list(tensors, dm_grad_t)[0] if len(tensors) else []
+    return _kept_array(tensors, dm_grad_t)
 
 
 def dm_grad_clip_workspace_size(tensors):

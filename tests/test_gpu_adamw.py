@@ -419,6 +419,22 @@ def test_on_another_stream():
     check_fp32(*h, hp, 1, to_host(W), to_host(st[0]), to_host(st[1]), F32)
 
 
+def test_descriptors_keep_their_tensors():
+    """Moments made in the descriptor's call live as long as the descriptors:
+    memory allocated afterwards is other memory."""
+    W, G = torch.zeros(5000, device="cuda"), torch.ones(5000, device="cuda")
+    for state in (dm.DM_STATE_FP32, dm.DM_STATE_8BIT):
+        for ts in ([dm.dm_adamw_tensor(W, G, *dm.dm_adamw_state(W, state))],
+                   dm.dm_adamw_tensors([dm.dm_adamw_tensor(W, G, *dm.dm_adamw_state(W, state))])):
+            used = {ts[0].moment1, ts[0].moment2, ts[0].scale1, ts[0].scale2}
+            fresh = [torch.empty(n, dtype=torch.uint8, device="cuda")
+                     for n in (1024, 5000, 20000, 160) * 8]
+            assert not used & {t.data_ptr() for t in fresh}
+    cl = dm.dm_grad_tensors([dm.dm_grad_tensor(torch.ones(5000, device="cuda"))])
+    assert cl[0].grad not in {torch.empty(20000, dtype=torch.uint8, device="cuda").data_ptr()
+                              for _ in range(4)}
+
+
 def test_nothing_to_do():
     hp = dm.dm_adamw_default_hparams()
     for ts in ([], [dm.dm_adamw_tensor(*(torch.zeros(0, device="cuda") for _ in range(4)))]):
