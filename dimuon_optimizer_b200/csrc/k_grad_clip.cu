@@ -148,8 +148,15 @@ template <int DT, int ODT, int K, int B>
 __device__ __forceinline__ void tile_write(const void* G, void* out, const Tile& t, bool vec, float c) {
   const char* base = elem_ptr<DT>(G, t.first);
   char* dst = elem_ptr<ODT>(out, t.first);
-  if (!vec) {
-    for (int i = threadIdx.x; i < t.hi; i += THREADS) st_elem(dst, i, ODT, ld_elem(base, i, DT) * c);
+  if (!vec) {  // another offset than the gradient's: element by element, eight in flight
+    for (int i = threadIdx.x; i < t.hi; i += 8 * THREADS) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = i + q * THREADS < t.hi ? ld_elem(base, i + q * THREADS, DT) : 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i + q * THREADS < t.hi) st_elem(dst, i + q * THREADS, ODT, v[q] * c);
+    }
     return;
   }
 #pragma unroll 1
