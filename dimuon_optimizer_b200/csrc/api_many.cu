@@ -124,7 +124,8 @@ uint8_t adamw_flags(const dm_adamw_tensor_t& t) {
     if (aligned(t.weight, 32) && aligned(t.grad, 32) && aligned(t.moment1, 16) &&
         aligned(t.moment2, 16))
       f |= MF_VEC;
-  } else if (offset_in(t.grad, gsz, 8) == s && offset_in(t.moment1, 4, 8) == s && offset_in(t.moment2, 4, 8) == s) {
+  } else if (offset_in(t.grad, gsz, 8) == s && offset_in(t.moment1, 4, 8) == s &&
+             offset_in(t.moment2, 4, 8) == s) {
     f |= MF_VEC | s << MF_SHIFT_BIT;
   }
   return (uint8_t)f;

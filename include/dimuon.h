@@ -305,9 +305,10 @@ dm_status_t dm_step_noalloc(const dm_matrix_t* mats, int n,
  * Conventions as above, and:
  *   - A tensor is `numel` contiguous elements; numel = 0 is allowed (its
  *     pointers are ignored).  Pointers need the alignment of their element
- *     type only; buffers whose addresses are at the same element offset from
- *     a 32-byte boundary (all of them aligned, or views at one offset of flat
- *     buffers) take the vector path.
+ *     type only; a tensor whose buffers all lie at the same element offset from
+ *     a multiple of 8 elements (dm_grad_clip: 16), as aligned buffers and views
+ *     at one offset of flat buffers do, takes the vector path.  8-bit moments
+ *     take it when weight and grad lie on 32 bytes and the codes on 16.
  *   - No element may be written twice in one call, nor read as a gradient and
  *     written (but by a tensor of dm_grad_clip whose out is its own grad): such
  *     buffers are rejected with DM_ERR_INVALID_ARG when their addresses are
