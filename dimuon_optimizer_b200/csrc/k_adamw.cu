@@ -69,6 +69,11 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ F2 mul2_rz(F2 a, F2 b) {  // rounded towards zero
+  F2 r;
+  asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 // A sum of two products that stay rounded: as two separate additions, because
 // the assembler joins a packed product and a packed sum into one packed
 // multiply-add, their .rn and --fmad=false notwithstanding (it costs 1.5 %).
@@ -221,7 +226,9 @@ __global__ void __launch_bounds__(THREADS) adamw32_step(const __grid_constant__ 
 // code's: the code's bits then stand in the fp32 pattern 20 (21) places up, the
 // subnormal codes as fp32 subnormals, and the bits below are the remainder.
 // Adding noise to them and cutting them off takes the upper neighbour with the
-// remainder's probability.
+// remainder's probability.  A remainder finer than the subnormal pattern holds
+// is cut off, not rounded: the noise counts in 2^-16 of a code's step, so what
+// lies below the pattern's last place (2^-20 or 2^-21 of it) decides nothing.
 // Two factors, as their product leaves fp32 for large scales.
 constexpr float E4M3_TO_BITS = 7.52316384526264e-37f;   // 2^-120
 constexpr float E5M2_TO_BITS = 1.925929944387236e-34f;  // 2^-112
@@ -427,8 +434,8 @@ __global__ void __launch_bounds__(THREADS, 4)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int q = 4 * k + j;
-        const float2 xm = split(mul2(mul2(m[q / 2], f2(i1)), f2(E4M3_TO_BITS)));
-        const float2 xv = split(mul2(mul2(v[q / 2], f2(i2)), f2(E5M2_TO_BITS)));
+        const float2 xm = split(mul2_rz(mul2(m[q / 2], f2(i1)), f2(E4M3_TO_BITS)));
+        const float2 xv = split(mul2_rz(mul2(v[q / 2], f2(i2)), f2(E5M2_TO_BITS)));
         uint32_t h = h0 + (uint32_t)q * (MANY_GOLDEN * 0x7FEB352Du);
         h = (h ^ (h >> 15)) * 0x846CA68Bu;
         // the hash's last round, h ^= h >> 16, leaves the upper half: noise of the first moment
