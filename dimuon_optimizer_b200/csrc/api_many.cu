@@ -23,6 +23,8 @@ constexpr int64_t MAX_NUMEL = int64_t(1) << 40;
 constexpr int64_t ADAMW8_LONG = int64_t(1) << 24;
 constexpr int64_t MAX_TILES = (int64_t(1) << 31) - 1;  // CTAs of one launch
 
+constexpr float EPS_MIN = 0x1p-126f, EPS_MAX = 0x1p125f;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool finite_h(float v) { return std::isfinite(v); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -76,8 +78,11 @@ dm_status_t validate(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparams_
   const float scalars[] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay};
   for (float v : scalars)
     if (!finite_h(v)) return DM_ERR_INVALID_ARG;
-  if (hp->beta1 < 0.f || hp->beta1 >= 1.f || hp->beta2 < 0.f || hp->beta2 >= 1.f || hp->eps < 0.f)
+  if (hp->beta1 < 0.f || hp->beta1 >= 1.f || hp->beta2 < 0.f || hp->beta2 >= 1.f)
     return DM_ERR_INVALID_ARG;
+  // The divisor sqrt(v) + eps is eps where v = 0: it and its reciprocal have to be normal numbers
+  // (the kernels' reciprocal takes subnormal ones for zero, and 0 x infinity would be NaN).
+  if (hp->eps != 0.f && !(hp->eps >= EPS_MIN && hp->eps <= EPS_MAX)) return DM_ERR_INVALID_ARG;
   if (!hp->step_counter && hp->step < 1) return DM_ERR_INVALID_ARG;
   if (!aligned(hp->step_counter, 8) || !aligned(hp->lr_dev, 4) || !aligned(hp->grad_scale, 4))
     return DM_ERR_INVALID_ARG;

@@ -362,7 +362,8 @@ typedef struct {
 typedef struct {
   float lr;
   float beta1, beta2;   /* in [0, 1) */
-  float eps;            /* >= 0 */
+  float eps;            /* 0, or 2^-126 to 2^125.  With 0 an element whose moments
+                           are both zero is 0 / 0: its weight becomes NaN */
   float weight_decay;   /* decoupled */
   uint32_t seed;        /* DM_STATE_8BIT: of the stochastic rounding */
   int64_t step;         /* t, from 1 on; ignored with step_counter */

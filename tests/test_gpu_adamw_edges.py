@@ -1,4 +1,5 @@
-"""Edges of dm_adamw_step on the GPU: remainders next to the rounding's noise."""
+"""Edges of dm_adamw_step on the GPU: remainders next to the rounding's noise,
+the least and the largest eps."""
 import numpy as np
 import pytest
 import torch
@@ -6,7 +7,7 @@ import torch
 import dimuon_optimizer_b200 as dm
 from gpu_harness import to_host
 from oracle import adamw_oracle as ao
-from test_gpu_adamw import workspace
+from test_gpu_adamw import check_fp32, workspace
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
@@ -62,3 +63,20 @@ def test_subnormal_codes_round_by_their_whole_remainder():
         np.testing.assert_array_equal(to_host(st[3]), s2)
         np.testing.assert_array_equal(codes(st[0]), c1)
         np.testing.assert_array_equal(codes(st[1]), c2)
+
+
+@pytest.mark.parametrize("state", [dm.DM_STATE_FP32, dm.DM_STATE_8BIT])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 2.0 ** 125])
+def test_zero_gradients_at_the_limits_of_eps(state, eps):
+    """Elements that saw no gradient divide 0 by eps alone; the others follow the formula."""
+    n = 3000
+    rng = np.random.default_rng(42)
+    W0, G = rng.standard_normal((2, n)).astype(F32)
+    G[::3] = 0
+    W = torch.from_numpy(W0).cuda()
+    hp = dm.dm_adamw_default_hparams(eps=eps, weight_decay=0.0)
+    ts = [dm.dm_adamw_tensor(W, torch.from_numpy(G).cuda(), *dm.dm_adamw_state(W, state))]
+    dm.check(dm.dm_adamw_step(ts, hp, workspace(ts, hp)))
+    z = np.zeros(n)
+    check_fp32(W0.astype(float), G.astype(float), z, z, hp, 1, to_host(W), None, None, torch.float32)
+    assert np.array_equal(to_host(W)[::3], W0[::3])
