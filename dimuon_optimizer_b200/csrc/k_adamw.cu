@@ -241,6 +241,14 @@ __device__ __forceinline__ void block_scale(uint32_t bits, int top, float& s, fl
   inv = __uint_as_float((uint32_t)(254 - e) << 23);
 }
 
+// 1.75 x 2^127, the largest second moment that is stored (the code above it would
+// stand for 2^128, which fp32 does not hold).  Larger ones, and one that
+// overflowed while the block's first moments did not (a finite gradient above
+// 1.8e19, whose square leaves fp32), are held there, so that the block stays
+// finite: the scale is that of HELD_BITS, and codes above LARGEST_E5M2 become it.
+constexpr uint32_t HELD_BITS = 0x7f600000u;
+constexpr uint32_t LARGEST_E5M2 = 0x7b7b7b7bu;  // four codes of 57344
+
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {  // over 8 neighbouring lanes
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -423,9 +431,11 @@ __global__ void __launch_bounds__(THREADS, 4)
       w.set(q, fma2(mul2(m[q], nstep), f2(rcp_ftz(d.x), rcp_ftz(d.y)), mul2(w.pair(q), decay)));
     }
     w.store(W, e, cnt, vec);
+    const uint32_t max1 = group_max(__float_as_uint(top1)), max2 = group_max(__float_as_uint(top2));
+    const bool held = max2 > HELD_BITS && max2 <= 0x7f800000u && max1 < 0x7f800000u;
     float i1, i2;
-    block_scale(group_max(__float_as_uint(top1)), 8, s1, i1);
-    block_scale(group_max(__float_as_uint(top2)), 15, s2, i2);
+    block_scale(max1, 8, s1, i1);
+    block_scale(held ? HELD_BITS : max2, 15, s2, i2);
     const uint32_t h0 = many_mix(key ^ e / 16) * 0x7FEB352Du;
     uint32_t zero = 0;
 #pragma unroll
@@ -458,6 +468,10 @@ __global__ void __launch_bounds__(THREADS, 4)
         if ((q & 1 ? f.y : f.x) > 0.f && (cv.w[q / 4] >> (8 * (q % 4)) & 0xffu) == 0)
           cv.w[q / 4] |= 1u << (8 * (q % 4));
       }
+    }
+    if (held) {  // an infinite moment gave 0xfc, a finite one above the largest 0x7b or 0x7c
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cv.w[k] = __vminu4(cv.w[k], LARGEST_E5M2);
     }
     cm.store(M, e, cnt, vec);
     cv.store(V, e, cnt, vec);

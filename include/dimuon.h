@@ -330,8 +330,15 @@ dm_status_t dm_step_noalloc(const dm_matrix_t* mats, int n,
  *   step, position of the tensor in the call, element), and the average of
  *   what is stored is the value.  A positive second moment is never rounded
  *   to zero (its element's next update would be divided by eps alone).
- *     A block with an infinite or NaN moment gets a NaN scale: the whole block
- *   stands for NaN from then on, as its element would in DM_STATE_FP32.    */
+ *     Where the gradient is infinite or NaN, the block gets NaN scales: all of
+ *   it stands for NaN from then on, as that element would in DM_STATE_FP32.
+ *     Second moments are stored as at most 1.75 x 2^127, also one that overflows
+ *   beside finite first moments (the square of a gradient above 1.8e19): it
+ *   decays from there, while in DM_STATE_FP32 it stays infinite and that weight
+ *   gets no update any more.  Meanwhile its block's scale makes the least
+ *   positive second moment of the 127 others 2^96, so they hardly move: clip
+ *   such gradients before.  A first moment above 1.75 x 2^127 may be stored as
+ *   2^128, infinite to who multiplies in fp32; the step takes its part of it. */
 typedef enum { DM_STATE_FP32 = 0, DM_STATE_8BIT = 1 } dm_state_t;
 
 #define DM_ADAMW_BLOCK 128

@@ -135,9 +135,19 @@ def noise(seed, t, tensor, n, first=0):
            (x % np.uint64(65536)).astype(np.float64) / 65536
 
 
+LARGEST = 1.75 * 2.0 ** 127  # second moment that is stored
+
+
+def hold(m, v):
+    """v as it is stored: up to LARGEST, also an infinite one beside a finite m
+    (a finite gradient whose square overflowed)."""
+    return np.where((np.asarray(v) > LARGEST) & np.isfinite(m), LARGEST, v)
+
+
 def pack_moments(m, v, seed, t, tensor):
     """(codes1, scales1, codes2, scales2) of the new moments; codes1 carries
     the sign in bit 7, and a positive v never gets code 0."""
+    v = hold(m, v)
     u1, u2 = noise(seed, t, tensor, len(m))
     s1, s2 = block_scales(m, 448.0), block_scales(v, 57344.0)
     c1 = stochastic_codes(m, s1, E4M3, u1) + 128 * np.signbit(m)

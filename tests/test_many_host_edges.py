@@ -1,8 +1,10 @@
 """Further host-side checks of the many-tensor entry points: what they refuse
 and what their sizes count, before anything is launched (no GPU needed)."""
+import numpy as np
 import pytest
 
 import dimuon_optimizer_b200 as dm
+from oracle import adamw_oracle as ao
 from test_many_host import fake_tensor
 
 
@@ -16,3 +18,14 @@ def test_an_eps_the_kernels_cannot_divide_by_is_refused():
             dm.dm_adamw_workspace_size([fake_tensor()], hp)
         # a step that were to run would find no workspace
         assert dm.dm_adamw_step([fake_tensor()], hp, (0, 0), stream=0) == dm.DM_ERR_INVALID_ARG
+
+
+def test_the_oracle_holds_second_moments_at_the_largest_code():
+    inf, nan, top = np.inf, np.nan, ao.LARGEST
+    m = np.array([1.0, 1.0, inf, nan, nan, 1.0, 1.0])
+    v = np.array([inf, 3.4e38, inf, inf, nan, nan, top])
+    np.testing.assert_array_equal(ao.hold(m, v), [top, top, inf, inf, nan, nan, top])
+    _, _, c2, s2 = ao.pack_moments(m[:2], v[:2], 1, 1, 0)
+    assert (c2 == 123).all() and s2[0] == 2.0 ** 112 and ao.unpack(c2, s2, ao.E5M2)[0] == top
+    # the next larger number of the format at that scale is none of fp32
+    assert 65536.0 * 2.0 ** 112 > float(np.finfo(np.float32).max)
