@@ -201,7 +201,7 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
   h.status = status;
   bool any = false;
   for (int i = 0; i < n; ++i) any = any || ts[i].numel > 0;
-  if (hp->step_counter) {
+  if (hp->step_counter || !any) {  // without elements, too, the status tells of the device values
     AdamwScalarsParams sp;
     sp.counter = hp->step_counter;
     sp.lr_dev = hp->lr_dev;
@@ -219,7 +219,6 @@ dm_status_t adamw_step(const dm_adamw_tensor_t* ts, int n, const dm_adamw_hparam
     h.sc.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow((double)hp->beta2, t)));
     h.sc.step_key = many_mix(hp->seed + MANY_GOLDEN * (uint32_t)hp->step);
     h.write_status = 1;
-    if (!any) DM_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
   }
 
   // one launch takes tensors of the same state format and types

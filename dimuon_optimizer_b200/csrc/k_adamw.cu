@@ -484,11 +484,13 @@ __global__ void __launch_bounds__(THREADS, 4)
 
 // ---------------------------------------------------------------------------
 // Step counted on the device: one thread looks at the device values, counts
-// the step and leaves what depends on it in the workspace.
+// the step and leaves what depends on it in the workspace.  Without a counter
+// (a host-counted step over no elements) it only writes the status.
 // ---------------------------------------------------------------------------
 __global__ void adamw_scalars(const AdamwScalarsParams p) {
   const bool skip = (p.grad_scale && !finite_f(*p.grad_scale)) || (p.lr_dev && !finite_f(*p.lr_dev));
   *p.status = skip ? ST_NONFINITE : ST_OK;
+  if (!p.counter) return;
   p.out->skip = skip;
   if (skip) return;
   const int64_t t = *p.counter + 1;

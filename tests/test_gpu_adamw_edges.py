@@ -1,5 +1,6 @@
 """Edges of dm_adamw_step on the GPU: remainders next to the rounding's noise,
-the least and the largest eps, moments at the end of fp32's range."""
+the least and the largest eps, moments at the end of fp32's range,
+steps over no elements."""
 import numpy as np
 import pytest
 import torch
@@ -168,3 +169,21 @@ def test_moments_at_the_end_of_fp32():
         for got, want in zip(st, (c1, c2, s1, s2)):
             np.testing.assert_array_equal(codes(got) if got.element_size() == 1 else to_host(got), want)
         assert (st[1].float() * st[3].repeat_interleave(128)).max().item() == ao.LARGEST
+
+
+@pytest.mark.parametrize("which", ["grad_scale", "lr_dev"])
+@pytest.mark.parametrize("counted", [False, True])
+def test_a_step_over_no_elements_reports_its_device_values(which, counted):
+    value = torch.tensor([float("nan")], device="cuda")
+    count = torch.tensor([4], dtype=torch.int64, device="cuda")
+    hp = dm.dm_adamw_default_hparams(**{which: value}, **({"step_counter": count} if counted else {}))
+    empty = [dm.dm_adamw_tensor(*(torch.zeros(0, device="cuda") for _ in range(4)))]
+    for ts in ([], empty):
+        value.fill_(float("nan"))
+        ws = workspace(ts, hp)
+        dm.check(dm.dm_adamw_step(ts, hp, ws))
+        assert dm.dm_read_device_status(ws) == dm.DM_ERR_NONFINITE and count.item() == 4
+        value.fill_(0.5)
+        dm.check(dm.dm_adamw_step(ts, hp, ws))
+        assert dm.dm_read_device_status(ws) == dm.DM_OK and count.item() == (5 if counted else 4)
+        count.fill_(4)
