@@ -21,7 +21,8 @@ constexpr int64_t MAX_NUMEL = int64_t(1) << 40;
 // From this many elements on, a CTA takes four passes of one tensor (there are
 // then seven CTAs and more for each SM).
 constexpr int64_t ADAMW8_LONG = int64_t(1) << 24;
-constexpr int64_t MAX_TILES = (int64_t(1) << 31) - 1;  // CTAs of one launch
+// Tiles of one launch: the norm pass steps by its grid, one step past the last tile too.
+constexpr int64_t MAX_TILES = (int64_t(1) << 31) - 1 - CLIP_MAX_GRID;
 
 constexpr float EPS_MIN = 0x1p-126f, EPS_MAX = 0x1p125f;
 

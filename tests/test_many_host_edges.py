@@ -5,7 +5,7 @@ import pytest
 
 import dimuon_optimizer_b200 as dm
 from oracle import adamw_oracle as ao
-from test_many_host import fake_tensor
+from test_many_host import fake_grad, fake_tensor
 
 
 def test_an_eps_the_kernels_cannot_divide_by_is_refused():
@@ -29,3 +29,22 @@ def test_the_oracle_holds_second_moments_at_the_largest_code():
     assert (c2 == 123).all() and s2[0] == 2.0 ** 112 and ao.unpack(c2, s2, ao.E5M2)[0] == top
     # the next larger number of the format at that scale is none of fp32
     assert 65536.0 * 2.0 ** 112 > float(np.finfo(np.float32).max)
+
+
+def test_tile_numbers_of_a_norm_launch_stay_within_32_bits():
+    """A CTA of the norm pass goes from tile to tile in steps of the grid (1184
+    at most), up to one step past the last: a launch's tiles end that far below 2^31.
+    (One gradient may be listed often, so lists longer than the memory are calls.)"""
+    tile, grid = 256 * 16 * 4, 1184
+    full = (1 << 40) // tile + 1  # tiles of the longest tensor, at any offset
+    rest = (1 << 31) - 31 * full
+    header = dm.dm_grad_clip_workspace_size([])
+
+    def launches(total):
+        ts = [fake_grad(numel=1 << 40)] * 31 + [fake_grad(numel=(total - 31 * full) * tile - 15)]
+        return (dm.dm_grad_clip_workspace_size(ts) - header) // (8 * grid)
+
+    assert 0 < rest < full
+    assert launches((1 << 31) - 1 - grid) == 1
+    for total in ((1 << 31) - grid, (1 << 31) - 1):
+        assert launches(total) == 2
