@@ -212,7 +212,28 @@ def _kept_array(items, struct):
         return []
     arr, _ = _list(items, struct)
     arr._keep = [getattr(t, "_keep", None) for t in items]
+    arr._devices = _devices_of(items)
     return arr
+
+
+def _devices_of(items):
+    """The devices that descriptors, or a kept array of them, hold addresses of
+    (none where they were filled by hand)."""
+    if isinstance(items, ctypes.Array):
+        return getattr(items, "_devices", ())
+    return {t._device for t in items if getattr(t, "_device", None) is not None}
+
+
+def _check_devices(devices, here):
+    """ValueError unless all of `devices` are `here`, the current CUDA device
+    (None: asked for where there is something to compare): a kernel launched on
+    one device with another's addresses would fault."""
+    for d in devices:
+        if here is None:
+            import torch
+            here = torch.cuda.current_device()
+        if d != here:
+            raise ValueError(f"tensors on cuda:{d}: needs the current CUDA device, cuda:{here}")
 
 
 def _stream_handle(stream):
@@ -379,6 +400,7 @@ def dm_adamw_tensor(weight, grad, moment1, moment2, scale1=None, scale2=None, lr
     t.moment1, t.moment2 = moment1.data_ptr(), moment2.data_ptr()
     t.lr_mult, t.decay_mult = lr_mult, decay_mult
     t._keep = (weight, grad, moment1, moment2, scale1, scale2)
+    t._device = weight.device.index
     return t
 
 
@@ -403,6 +425,7 @@ def dm_adamw_default_hparams(**overrides):
                 raise ValueError(f"{k} must be one {want} element on the device")
             _on_device(v)
             hp._keep.append(v)
+            hp._devices = (v.device.index,)
             v = v.data_ptr()
         setattr(hp, k, v)
     return hp
@@ -420,8 +443,14 @@ def dm_adamw_workspace_size(tensors, hp):
 def dm_adamw_step(tensors, hp, workspace, stream=None):
     """One AdamW step over the tensors (include/dimuon.h).  The caller counts
     the steps in hp.step, or gives hp a device step_counter."""
+    here = None
     if hasattr(workspace, "data_ptr"):
         _on_device(workspace)
+        here = workspace.device.index
+    if not isinstance(tensors, ctypes.Array):
+        tensors = list(tensors)
+    _check_devices(_devices_of(tensors), here)
+    _check_devices(getattr(hp, "_devices", ()), here)
     arr, n = _list(tensors, dm_adamw_tensor_t)
     ptr, nbytes = _ws(workspace)
     return _lib.dm_adamw_step(arr, n, ctypes.byref(hp), ptr, nbytes, _stream_handle(stream))
@@ -439,6 +468,7 @@ def dm_grad_tensor(grad, out=None):
         t.out, t.out_dtype = out.data_ptr(), _dtype_code(out)
     _on_device(grad, out)
     t._keep = (grad, out)
+    t._device = grad.device.index
     return t
 
 
@@ -463,6 +493,9 @@ def dm_grad_clip(tensors, max_norm, result, workspace, stream=None):
     if result.numel() != 2 or result.dtype != torch.float32:
         raise ValueError("result must be an fp32 tensor of two elements")
     _on_device(result, workspace if hasattr(workspace, "data_ptr") else None)
+    if not isinstance(tensors, ctypes.Array):
+        tensors = list(tensors)
+    _check_devices(_devices_of(tensors), result.device.index)
     arr, n = _list(tensors, dm_grad_t)
     ptr, nbytes = _ws(workspace)
     return _lib.dm_grad_clip(arr, n, float(max_norm), c_void_p(result.data_ptr()), ptr, nbytes,
