@@ -431,8 +431,12 @@ dm_status_t dm_grad_clip_workspace_size(const dm_grad_t* tensors, int n, size_t*
  *   result[1] = min(1, max_norm / result[0])   (1 for a zero norm)
  *   out       = grad * result[1], rounded to nearest even
  * `result` is a DEVICE float[2]; max_norm > 0 (INFINITY: the norm only, out
- * is a copy).  The sum is taken in a fixed order (the same inputs give the
- * same bits), with squares that leave fp32's range taken in fp64.
+ * is a copy).  The order of the sum goes by the list, the lengths and each
+ * gradient's offset from a multiple of 16 elements: the same values in buffers
+ * that lie alike give the same bits, in every run; at another offset the last
+ * bit may be another one, so replicas that have to agree bit for bit keep
+ * their gradients at the same offsets (or share one rank's result).  Squares
+ * that leave fp32's range are taken in fp64.
  * Where the norm is not finite in fp32, result[0] holds it (inf or NaN), result[1]
  * is NaN, no `out` is written and the device status reads DM_ERR_NONFINITE;
  * dm_adamw_step given that result[1] as grad_scale skips its step.
