@@ -418,7 +418,10 @@ def dm_adamw_default_hparams(**overrides):
     hp = dm_adamw_hparams_t()
     _lib.dm_adamw_default_hparams(ctypes.byref(hp))
     hp._keep = []
+    fields = [name for name, _ in dm_adamw_hparams_t._fields_]
     for k, v in overrides.items():
+        if k not in fields:  # setattr would take it, and the step would go on without
+            raise TypeError(f"dm_adamw_hparams_t has no field {k!r}: one of {', '.join(fields)}")
         if k in ("step_counter", "lr_dev", "grad_scale") and v is not None:
             want = torch.int64 if k == "step_counter" else torch.float32
             if v.numel() != 1 or v.dtype != want:

@@ -132,3 +132,11 @@ def test_a_generator_of_descriptors_is_one_list(devices):
     gen = (dm.dm_adamw_tensor(*(OnDevice(0) for _ in range(4))) for _ in range(3))
     dm.dm_adamw_step(gen, dm.dm_adamw_default_hparams(), WS, stream=0)
     assert got == [3]
+
+
+def test_hyper_parameters_of_other_names_are_refused():
+    """torch's betas=(0.9, 0.95), say, must not leave the defaults in place."""
+    for name in ("betas", "wd", "Lr", "_keep"):
+        with pytest.raises(TypeError, match="no field"):
+            dm.dm_adamw_default_hparams(**{name: (0.9, 0.95)})
+    assert dm.dm_adamw_default_hparams(seed=3, step_counter=None).seed == 3
