@@ -236,14 +236,15 @@ def _check_devices(devices, here):
             raise ValueError(f"tensors on cuda:{d}: needs the current CUDA device, cuda:{here}")
 
 
-def _stream_handle(stream):
+def _stream_handle(stream, here=None):
+    """`here`: the current device, where the caller has asked for it already."""
     if stream is None:
         import torch
         # the handle itself: making a Stream object of it takes 3 us more, as
         # long as the launch of a small step
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return c_void_p(raw(torch.cuda.current_device()))
+            return c_void_p(raw(torch.cuda.current_device() if here is None else here))
         return c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return c_void_p(stream)
@@ -337,15 +338,19 @@ def dm_step_noalloc(mats, hp, conditioned, device_status_out=None, stream=None):
 # ----------------------------------------------------------------------------
 def _on_device(*tensors):
     """All on the current CUDA device and contiguous, else ValueError (a host
-    or foreign address would fault in the kernels)."""
+    or foreign address would fault in the kernels).  Returns that device."""
     import torch
+    here = None
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        if here is None and t.is_cuda:
+            here = torch.cuda.current_device()
+        if not t.is_cuda or t.device.index != here:
             raise ValueError(f"tensor on {t.device}: needs the current CUDA device")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+    return here
 
 
 def dm_adamw_state(weight, state=DM_STATE_FP32):
@@ -394,13 +399,12 @@ def dm_adamw_tensor(weight, grad, moment1, moment2, scale1=None, scale2=None, lr
     else:
         raise TypeError(f"unsupported moments {kinds} (fp32, or float8_e4m3fn and float8_e5m2)")
     t.weight_dtype, t.grad_dtype = _dtype_code(weight), _dtype_code(grad)
-    _on_device(weight, grad, moment1, moment2, scale1, scale2)
+    t._device = _on_device(weight, grad, moment1, moment2, scale1, scale2)
     t.numel = n
     t.weight, t.grad = weight.data_ptr(), grad.data_ptr()
     t.moment1, t.moment2 = moment1.data_ptr(), moment2.data_ptr()
     t.lr_mult, t.decay_mult = lr_mult, decay_mult
     t._keep = (weight, grad, moment1, moment2, scale1, scale2)
-    t._device = weight.device.index
     return t
 
 
@@ -426,9 +430,8 @@ def dm_adamw_default_hparams(**overrides):
             want = torch.int64 if k == "step_counter" else torch.float32
             if v.numel() != 1 or v.dtype != want:
                 raise ValueError(f"{k} must be one {want} element on the device")
-            _on_device(v)
+            hp._devices = (_on_device(v),)
             hp._keep.append(v)
-            hp._devices = (v.device.index,)
             v = v.data_ptr()
         setattr(hp, k, v)
     return hp
@@ -446,17 +449,14 @@ def dm_adamw_workspace_size(tensors, hp):
 def dm_adamw_step(tensors, hp, workspace, stream=None):
     """One AdamW step over the tensors (include/dimuon.h).  The caller counts
     the steps in hp.step, or gives hp a device step_counter."""
-    here = None
-    if hasattr(workspace, "data_ptr"):
-        _on_device(workspace)
-        here = workspace.device.index
+    here = _on_device(workspace) if hasattr(workspace, "data_ptr") else None
     if not isinstance(tensors, ctypes.Array):
         tensors = list(tensors)
     _check_devices(_devices_of(tensors), here)
     _check_devices(getattr(hp, "_devices", ()), here)
     arr, n = _list(tensors, dm_adamw_tensor_t)
     ptr, nbytes = _ws(workspace)
-    return _lib.dm_adamw_step(arr, n, ctypes.byref(hp), ptr, nbytes, _stream_handle(stream))
+    return _lib.dm_adamw_step(arr, n, ctypes.byref(hp), ptr, nbytes, _stream_handle(stream, here))
 
 
 def dm_grad_tensor(grad, out=None):
@@ -469,9 +469,8 @@ def dm_grad_tensor(grad, out=None):
     t.numel, t.grad, t.grad_dtype = grad.numel(), grad.data_ptr(), _dtype_code(grad)
     if out is not None:
         t.out, t.out_dtype = out.data_ptr(), _dtype_code(out)
-    _on_device(grad, out)
+    t._device = _on_device(grad, out)
     t._keep = (grad, out)
-    t._device = grad.device.index
     return t
 
 
@@ -495,14 +494,14 @@ def dm_grad_clip(tensors, max_norm, result, workspace, stream=None):
     import torch
     if result.numel() != 2 or result.dtype != torch.float32:
         raise ValueError("result must be an fp32 tensor of two elements")
-    _on_device(result, workspace if hasattr(workspace, "data_ptr") else None)
+    here = _on_device(result, workspace if hasattr(workspace, "data_ptr") else None)
     if not isinstance(tensors, ctypes.Array):
         tensors = list(tensors)
-    _check_devices(_devices_of(tensors), result.device.index)
+    _check_devices(_devices_of(tensors), here)
     arr, n = _list(tensors, dm_grad_t)
     ptr, nbytes = _ws(workspace)
     return _lib.dm_grad_clip(arr, n, float(max_norm), c_void_p(result.data_ptr()), ptr, nbytes,
-                             _stream_handle(stream))
+                             _stream_handle(stream, here))
 
 
 def dm_read_device_status(workspace, stream=None):
