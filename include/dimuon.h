@@ -440,6 +440,10 @@ dm_status_t dm_grad_clip_workspace_size(const dm_grad_t* tensors, int n, size_t*
  * Where the norm is not finite in fp32, result[0] holds it (inf or NaN), result[1]
  * is NaN, no `out` is written and the device status reads DM_ERR_NONFINITE;
  * dm_adamw_step given that result[1] as grad_scale skips its step.
+ * dm_muon_step and dm_dimuon_step have no such skip: a NaN in a gradient goes
+ * into that matrix's momentum and stays, and the other matrices step on
+ * gradients that were not clipped.  Read the status before calling them, and
+ * capture them, if at all, in another graph than the clipping.
  * An `out` that is `grad` itself is not rewritten when result[1] = 1.
  * Asynchronous on `stream`. */
 dm_status_t dm_grad_clip(const dm_grad_t* tensors, int n, float max_norm,
