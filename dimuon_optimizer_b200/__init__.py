@@ -410,7 +410,9 @@ def dm_adamw_tensor(weight, grad, moment1, moment2, scale1=None, scale2=None, lr
 
 def dm_adamw_tensors(tensors):
     """The descriptors as one C array, for callers that keep it from step to
-    step (a plain list is converted at every call)."""
+    step (a plain list is converted at every call).  It holds addresses, and
+    keeps the tensors behind them: gradients have to stay in their buffers
+    (zero_grad(set_to_none=False)), else the steps go on with the old ones."""
     return _kept_array(tensors, dm_adamw_tensor_t)
 
 
@@ -475,7 +477,8 @@ def dm_grad_tensor(grad, out=None):
 
 
 def dm_grad_tensors(tensors):
-    """The descriptors as one C array, for callers that keep it."""
+    """The descriptors as one C array, for callers that keep it (and leave the
+    gradients in their buffers: see dm_adamw_tensors)."""
     return _kept_array(tensors, dm_grad_t)
 
 

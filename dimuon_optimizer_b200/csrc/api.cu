@@ -1014,7 +1014,7 @@ const char* dm_status_string(int32_t status) {
     case DM_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case DM_ERR_CUDA: return "CUDA call failed";
     case DM_ERR_DEVICE_TIMEOUT: return "device wait timed out";
-    case DM_ERR_NONFINITE: return "non-finite Frobenius norm (update set to zero)";
+    case DM_ERR_NONFINITE: return "non-finite norm or device value (no update from it)";
     case DM_ERR_CANARY: return "workspace canary overwritten";
     default: return "unknown status";
   }

@@ -19,7 +19,7 @@ constexpr size_t HEADER_BYTES = 1024;      // status word at 0, AdamwScalars at 
 constexpr size_t SCALARS_OFFSET = 64;
 constexpr int64_t MAX_NUMEL = int64_t(1) << 40;
 // From this many elements on, a CTA takes four passes of one tensor (there are
-// then seven CTAs and more for each SM).
+// then 1024 CTAs and more, 6.9 for each SM; both sides measured at adamw8_step).
 constexpr int64_t ADAMW8_LONG = int64_t(1) << 24;
 // Tiles of one launch: the norm pass steps by its grid, one step past the last tile too.
 constexpr int64_t MAX_TILES = (int64_t(1) << 31) - 1 - CLIP_MAX_GRID;

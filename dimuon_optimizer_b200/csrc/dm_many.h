@@ -99,7 +99,9 @@ cudaError_t launch_adamw8(const Adamw8Params<N>& p, int wdt, int gdt, int grid, 
 cudaError_t launch_adamw_scalars(const AdamwScalarsParams& p, cudaStream_t s);
 
 // The 32-bit mixing step of the rounding's hash (host and device): two
-// multiply and shift rounds, a bijection.
+// multiply and shift rounds, a bijection.  Shifts and multipliers are the
+// published ones of least measured bias for that form (C. Wellons, "Prospecting
+// for Hash Functions", 2018).
 __host__ __device__ inline uint32_t many_mix(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x7FEB352Du;
   x = (x ^ (x >> 15)) * 0x846CA68Bu;

@@ -356,21 +356,24 @@ struct Codes16 {
 };
 
 // Bound by HBM up to the power limit: 262 M elements (bf16 weights and
-// gradients) take 396 us (6.72 TB/s) while the clock stays at 1.96 GHz, 447 us
-// (0.91 of the measured copy) in a long run, when the part reaches its 1000 W
-// and the clock falls to 1.6 GHz: 40 instructions per element then fill three
-// quarters of the issue slots.  The first form (one fp32 operation at a time,
-// separate code for the subnormal codes, one pass per CTA) took 88 instructions
-// and 837 us.  Packed fp32 arithmetic, the codes' bits by a power-of-two
-// product, the packed fp8 conversions and the test for zero codes four at a
-// time brought that down.  A CTA takes four passes, so that finding its tensor
-// and the coefficients costs little (2 passes: 466 us; 8: 444 us, but 152
-// instead of 142 us on 448 tensors of 131072 elements).  Reading the next pass
-// into registers during this one made it twice as slow (128 registers).
-// Registers are held to 64, four CTAs per SM (without the limit 66 to 104 by
-// type: 458 instead of 449 us, and 182 instead of 173 us with 66 M fp32 weights
-// and gradients).  Accesses of 32 bytes instead of 16 gave the last 7 % (449 to 418 us).
-// FLUSH: see sqrt_approx (447 against 465 us in the long run; with fp32 moments the
+// gradients) take 397 us (6.71 TB/s) while the clock stays at 1.96 GHz, and 424 to
+// 455 us by the board (0.96 to 0.89 of the measured copy) in a long run, when the
+// part reaches its 1000 W and the clock falls to 1.6 GHz: 41.5 instructions per
+// element then fill four fifths of the issue slots.  The first form (one
+// fp32 operation at a time, separate code for the subnormal codes, one pass
+// per CTA) took 88 instructions and 837 us.  Packed fp32 arithmetic, the codes'
+// bits by a power-of-two product, the packed fp8 conversions and the test for
+// zero codes four at a time brought that down, and accesses of 32 bytes instead of
+// 16 by another 7 %.  What follows was measured against each other in long runs.
+// A CTA takes four passes, so that finding its tensor and the coefficients
+// costs little (2 passes: 466 us, 4: 446, 8: 444, but with 8 152 instead of 142
+// us on 448 tensors of 131072 elements); lists of less than 2^24 elements take
+// one, as four would leave fewer than 1024 CTAs for the 592 that are resident.  Reading the next
+// pass into registers during this one made it twice as slow (128 registers).
+// Registers are held to 64, four CTAs per SM; 21 of the 24 forms spill one or
+// two of them for that (without the limit 66 to 104 by type: 458 instead of 449
+// us, and 182 instead of 173 us with 66 M fp32 weights and gradients).
+// FLUSH: see sqrt_approx (447 against 465 us; with fp32 moments the
 // instructions are hidden behind HBM, so that form has no such variant).
 template <int N, int WDT, int GDT, bool FLUSH>
 __global__ void __launch_bounds__(THREADS, 4)

@@ -12,7 +12,9 @@
 // into bf16 take 152 us: read twice and written once that is 6.6 TB/s.  What
 // was tried beyond: L2 eviction hints that keep the norm pass's last 64 MB
 // (153 us); short lists in one launch of one cluster, with the sums exchanged
-// through distributed shared memory (98 vectors of 768: 5.2 us, two launches 4.3).
+// through distributed shared memory (98 vectors of 768: 5.2 us on the device, two
+// launches 4.3; a call takes 11.5 to 13.6 us, most of it the host's two
+// launches, and by that measure the two forms were not compared).
 #include "dm_common.cuh"
 #include "dm_many.h"
 

@@ -375,7 +375,7 @@ typedef struct {
   uint32_t seed;        /* DM_STATE_8BIT: of the stochastic rounding */
   int64_t step;         /* t, from 1 on; ignored with step_counter */
   int64_t* step_counter;  /* NULL, or a DEVICE int64: the number of steps
-                             done.  The step runs as t = *step_counter + 1 and
+                             done, 0 or more.  The step runs as t = *step_counter + 1 and
                              stores that, so that a captured graph counts its
                              own replays.  Not advanced by a skipped step. */
   const float* lr_dev;  /* NULL, or a DEVICE float read in place of lr      */
@@ -403,7 +403,8 @@ dm_status_t dm_adamw_workspace_size(const dm_adamw_tensor_t* tensors, int n,
  *   W' = (1 - lr wd) W - lr (m' / (1 - beta1^t)) /
  *                        (sqrt(v' / (1 - beta2^t)) + eps)
  * (lr and wd with the tensor's multipliers; W' comes from m' and v' before
- * they are rounded to 8 bits).  Asynchronous on `stream`.
+ * they are rounded to 8 bits; in DM_STATE_8BIT beta x scale is taken first, which
+ * changes no bit unless that product is below 2^-126: beta below 2^-16).  Asynchronous on `stream`.
  * When the device value of grad_scale or lr_dev is not finite, the step is
  * skipped: nothing but the device status is written, and that reads
  * DM_ERR_NONFINITE (dm_read_device_status).  Non-finite gradients are not

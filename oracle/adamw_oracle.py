@@ -111,6 +111,7 @@ def stochastic_codes(x, scales, table, u):
 
 
 def mix(x):
+    """A bijection of 32-bit words (C. Wellons, "Prospecting for Hash Functions", 2018)."""
     x = np.asarray(x, np.uint64)
     x = ((x ^ (x >> np.uint64(16))) * np.uint64(0x7FEB352D)) % np.uint64(2 ** 32)
     x = ((x ^ (x >> np.uint64(15))) * np.uint64(0x846CA68B)) % np.uint64(2 ** 32)
